@@ -84,7 +84,9 @@ typedef enum {
     SLAY_OP_LINEAR_ATTN = 6,    /* slay_linear_attn_fwd: R * m = the number of features */
     SLAY_OP_CAUSAL_STATE = 7,   /* slay_causal_state */
     SLAY_OP_CAUSAL_FWD_SPLIT = 8, /* slay_attn_causal_fwd_begin / _finish (one workspace) */
-    SLAY_OP_FEATURE_MAP_BWD = 9  /* slay_feature_map_bwd (no workspace; for slay_path) */
+    SLAY_OP_FEATURE_MAP_BWD = 9, /* slay_feature_map_bwd (no workspace; for slay_path) */
+    SLAY_OP_DECAY_FWD = 10,     /* slay_decay_attn_fwd: R * m = the number of features */
+    SLAY_OP_DECAY_BWD = 11      /* slay_decay_attn_bwd, likewise */
 } slay_op;
 
 /* Feature-map variants (slay_feature_map_ex).  The pages leave the form of the anchor
@@ -337,6 +339,89 @@ slay_status slay_linear_attn_fwd(const void* phq, const void* phk, const void* v
                                  float* den, int B, int H, int L, int F, int Dv, slay_dtype dt,
                                  float eps, int causal, void* workspace, size_t ws_bytes,
                                  void* stream);
+
+/* The linear-attention contraction on given features with a decay for each head: the causal
+ * contraction of slay_linear_attn_fwd in which a token's weight falls by lambda = exp(log_decay)
+ * with every later token (lambda^0 = 1; log_decay <= 0, -inf gives lambda = 0).  Over the
+ * tokens 0 .. n-1 of a sequence:
+ *   num_i = sum_{j<=i} lambda^(i-j) (phq_i . phk_j) v_j + lambda^(i+1) phq_i^T S_in
+ *   den_i = sum_{j<=i} lambda^(i-j) (phq_i . phk_j)     + lambda^(i+1) phq_i . z_in
+ *   out_i = num_i / (den_i + eps) if normalize != 0, else num_i
+ *   S_out = sum_j lambda^(n-1-j) phk_j v_j^T + lambda^n S_in,
+ *   z_out = sum_j lambda^(n-1-j) phk_j       + lambda^n z_in
+ * in O(L), by chunks with fp32 states.  With log_decay = 0 and normalize != 0 it is
+ * slay_linear_attn_fwd(causal); normalize = 0 suits signed rows (plain queries and keys).
+ * phq, phk  : device [B,H,L,F] in dt;  v : device [B,H,L,Dv] in dt;  F <= 1024, Dv == 64.
+ * log_decay : device [H] fp32, a constant of the model (there is no gradient for it).
+ * lengths   : device [B] int32 or NULL (every sequence has L tokens): sequence b is its first
+ *             lengths[b] tokens (taken into [0, L]).  The inputs behind them do not matter,
+ *             whatever they hold, and the outputs behind them are left as they were.
+ * S_in, z_in, S_out, z_out : device [B,H,F,Dv], [B,H,F] fp32; S_in NULL: zero, S_out NULL: not
+ *             wanted.  z goes with S when normalize != 0 and is NULL when normalize == 0.
+ *             S_out, z_out may be S_in, z_in themselves.  A sequence of no tokens keeps its state.
+ * out : device [B,H,L,Dv] in dt;  den : device [B,H,L] fp32 or NULL (without eps; NULL when
+ *             normalize == 0).  eps is ignored when normalize == 0.
+ * workspace : slay_workspace_bytes(SLAY_OP_DECAY_FWD, dt, B, H, L, 64, Dv, 1, F) bytes. */
+slay_status slay_decay_attn_fwd(const void* phq, const void* phk, const void* v,
+                                const float* log_decay, const int32_t* lengths,
+                                const float* S_in, const float* z_in, void* out, float* den,
+                                float* S_out, float* z_out, int B, int H, int L, int F, int Dv,
+                                slay_dtype dt, int normalize, float eps, void* workspace,
+                                size_t ws_bytes, void* stream);
+
+/* Gradients of slay_decay_attn_fwd.  With rz_i = 1 / (den_i + eps), r_i = out_i . dout_i
+ * (normalize == 0: rz = 1, r = 0) and c_ij = rz_i (v_j . dout_i - r_i):
+ *   dphq_i = sum_{j<=i} lambda^(i-j) c_ij phk_j + lambda^(i+1) rz_i (S_in dout_i - r_i z_in)
+ *   dphk_j = sum_{i>=j} lambda^(i-j) c_ij phq_i + lambda^(n-1-j) (dS_out v_j + dz_out)
+ *   dv_j   = sum_{i>=j} lambda^(i-j) rz_i (phq_i . phk_j) dout_i + lambda^(n-1-j) dS_out^T phk_j
+ *   dS_in  = sum_i lambda^(i+1) rz_i phq_i dout_i^T + lambda^n dS_out
+ *   dz_in  = -sum_i lambda^(i+1) rz_i r_i phq_i + lambda^n dz_out
+ * phq, phk, v, log_decay, lengths, S_in, z_in : as the forward was given them.
+ * out, den   : the forward's (read when normalize != 0, else ignored); dout : [B,H,L,Dv] in dt.
+ * dS_out, dz_out : gradients of the final state, fp32, NULL: zero.
+ * dphq, dphk [B,H,L,F], dv [B,H,L,Dv] : written, in dt (slay_feature_map_bwd takes them); rows
+ *             behind a sequence are left as they were.
+ * dS_in, dz_in : fp32, NULL: not wanted; may be dS_out, dz_out themselves.
+ * workspace  : slay_workspace_bytes(SLAY_OP_DECAY_BWD, dt, B, H, L, 64, Dv, 1, F) bytes. */
+slay_status slay_decay_attn_bwd(const void* phq, const void* phk, const void* v,
+                                const float* log_decay, const int32_t* lengths,
+                                const float* S_in, const float* z_in, const void* out,
+                                const float* den, const void* dout, const float* dS_out,
+                                const float* dz_out, void* dphq, void* dphk, void* dv,
+                                float* dS_in, float* dz_in, int B, int H, int L, int F, int Dv,
+                                slay_dtype dt, int normalize, float eps, void* workspace,
+                                size_t ws_bytes, void* stream);
+
+/* One token of decayed linear attention for each of Bt running sequences whose states live in
+ * the slots of a pool, inclusive:
+ *   S <- lambda S + phk v^T;  z <- lambda z + phk;
+ *   out = phq^T S / (phq . z + eps) if normalize != 0, else phq^T S
+ * phq, phk : device [Bt,H,F] in dt;  v, out : device [Bt,H,Dv] in dt;  log_decay : [H] fp32.
+ * S, z  : device [n_slots,H,F,Dv], [n_slots,H,F] fp32, updated in place (z NULL when
+ *         normalize == 0).
+ * slots : device [Bt] int32 or NULL (row b steps slot b; Bt <= n_slots).  A row whose slot is
+ *         outside [0, n_slots), such as -1 for an idle row of the batch, is left out: nothing is
+ *         read or written for it, and its out row stays as it was.  So is a row whose slot an
+ *         earlier row of the call names.
+ * No workspace. */
+slay_status slay_decay_decode_step(const void* phq, const void* phk, const void* v,
+                                   const float* log_decay, float* S, float* z,
+                                   const int32_t* slots, void* out, int Bt, int H, int F, int Dv,
+                                   int n_slots, slay_dtype dt, int normalize, float eps,
+                                   void* stream);
+
+/* Copies n slots of states: slot dst[i] of the destination pool becomes slot src[i] of the
+ * source pool, or zero where src[i] is -1.  Every source is read as it was before the call, so
+ * in one pool slots may be forked, moved, swapped and cleared in one call; where dst names a
+ * slot more than once the last pair wins.
+ * S_src, z_src : device [n_src,H,F,Dv], [n_src,H,F] fp32;  S_dst, z_dst : likewise n_dst slots.
+ *         The two pools are one and the same or share no byte.  z_src, z_dst both NULL: no z.
+ * src, dst : device [n] int32, n <= 4096.  A pair with src outside [-1, n_src) or dst outside
+ *         [0, n_dst) is left out.
+ * No workspace. */
+slay_status slay_state_copy(const float* S_src, const float* z_src, const int32_t* src, int n_src,
+                            float* S_dst, float* z_dst, const int32_t* dst, int n_dst, int n,
+                            int H, int F, int Dv, void* stream);
 
 /* Backward of the feature map alone (review, "Proposed method", steps 1, 3, 4, 5; the
  * pages give no backward): dx = (d phi / d x)^T dphi for every row, through the sphere

@@ -18,7 +18,8 @@ SLAY_OK, SLAY_ERR_INVALID_ARG, SLAY_ERR_UNSUPPORTED, SLAY_ERR_CUDA, SLAY_ERR_TIM
     SLAY_ERR_NO_MEMORY = range(6)
 SLAY_F32, SLAY_BF16 = 0, 1
 OP_FEATURE_MAP, OP_CAUSAL_FWD, OP_BIDIR_FWD, OP_CAUSAL_BWD, OP_DECODE, OP_BIDIR_BWD, \
-    OP_LINEAR_ATTN, OP_CAUSAL_STATE, OP_CAUSAL_FWD_SPLIT, OP_FEATURE_MAP_BWD = range(10)
+    OP_LINEAR_ATTN, OP_CAUSAL_STATE, OP_CAUSAL_FWD_SPLIT, OP_FEATURE_MAP_BWD, OP_DECAY_FWD, \
+    OP_DECAY_BWD = range(12)
 PATH_TC_FEATURE_MAP, PATH_TC_CONTRACTION, PATH_TC_PHI_BWD = 1, 2, 4
 PHI_ANCHOR, PHI_ORTHOGONAL, PHI_SIGNED, PHI_PER_HEAD, PHI_PERFORMER = range(5)
 
@@ -31,7 +32,8 @@ EXPORTS = ["slay_feature_map", "slay_attn_causal_fwd", "slay_attn_bidir_fwd",
            "slay_attn_causal_fwd_state", "slay_causal_state", "slay_state_prefix",
            "slay_state_suffix", "slay_attn_causal_bwd_state", "slay_causal_bwd_state",
            "slay_attn_causal_fwd_begin", "slay_attn_causal_fwd_finish", "slay_path",
-           "slay_attn_causal_bwd_begin", "slay_attn_causal_bwd_finish"]
+           "slay_attn_causal_bwd_begin", "slay_attn_causal_bwd_finish", "slay_decay_attn_fwd",
+           "slay_decay_attn_bwd", "slay_decay_decode_step", "slay_state_copy"]
 
 
 class SlayError(RuntimeError):
@@ -86,6 +88,10 @@ def lib():
     L.slay_attn_causal_bwd_finish.argtypes = L.slay_attn_causal_bwd_state.argtypes
     L.slay_decode_step.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
                                    u64, f32, vp]
+    L.slay_decay_attn_fwd.argtypes = [vp] * 11 + [i32] * 7 + [f32, vp, sz, vp]
+    L.slay_decay_attn_bwd.argtypes = [vp] * 17 + [i32] * 7 + [f32, vp, sz, vp]
+    L.slay_decay_decode_step.argtypes = [vp] * 8 + [i32] * 7 + [f32, vp]
+    L.slay_state_copy.argtypes = [vp, vp, vp, i32, vp, vp, vp] + [i32] * 5 + [vp]
     L.slay_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32]
     L.slay_workspace_bytes.restype = sz
     L.slay_path.argtypes = [i32] * 9
@@ -112,7 +118,8 @@ def lib():
                  "slay_attn_causal_bwd_state", "slay_causal_bwd_state",
                  "slay_attn_causal_fwd_noalloc", "slay_attn_causal_fwd_begin",
                  "slay_attn_causal_fwd_finish", "slay_attn_causal_bwd_begin",
-                 "slay_attn_causal_bwd_finish",
+                 "slay_attn_causal_bwd_finish", "slay_decay_attn_fwd", "slay_decay_attn_bwd",
+                 "slay_decay_decode_step", "slay_state_copy",
                  "slay_sketch_params"):
         getattr(L, name).restype = i32
     _lib = L
@@ -589,3 +596,141 @@ def slay_decode_step(q, k, v, S, z, out, R, m, seed, eps, stream=None):
     _raise(lib().slay_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(S), _ptr(z), _ptr(out), Bt, H,
                                   D, Dv, _dt(q), R, m, seed, eps, _stream(stream)),
            "slay_decode_step")
+
+
+def _check_on(device, t, name, dtype=None, shape=None, optional=False):
+    """_check, on `device`; None passes where the argument is optional."""
+    if t is None and optional:
+        return
+    _check(t, name, dtype, shape)
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+
+
+def _stream_on(device, stream):
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    if s.device != device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (s.device, device))
+    return C.c_void_p(s.cuda_stream)
+
+
+def _decay_pair(device, S, z, shape, normalize, name):
+    """A state S [.., F, 64] and, in the normalized form, its z [.., F]; both may be None."""
+    _check_on(device, S, "S_" + name, torch.float32, shape + (64,), optional=True)
+    _check_on(device, z, "z_" + name, torch.float32, shape, optional=True)
+    if (z is not None) != (S is not None and normalize):
+        raise ValueError("z_%s goes with S_%s when normalized, and only then" % (name, name))
+
+
+def _decay_common(phq, phk, v, log_decay, lengths):
+    _check(phq, "phq")
+    if phq.dim() != 4 or v is None or v.dim() != 4:
+        raise ValueError("phq, phk are [B, H, L, F] and v is [B, H, L, Dv]")
+    B, H, L, F = phq.shape
+    dev = phq.device
+    _check_on(dev, phk, "phk", phq.dtype, (B, H, L, F))
+    _check_on(dev, v, "v", phq.dtype, (B, H, L, v.shape[-1]))
+    _check_on(dev, log_decay, "log_decay", torch.float32, (H,))
+    _check_on(dev, lengths, "lengths", torch.int32, (B,), optional=True)
+    return dev, B, H, L, F, v.shape[-1]
+
+
+def _decay_workspace(op, dt, B, H, L, F, Dv, workspace, dev):
+    if workspace is None:
+        workspace = alloc_workspace(op, dt, B, H, L, 64, Dv, 1, F, dev)
+    _check_on(dev, workspace, "workspace")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def slay_decay_attn_fwd(phq, phk, v, log_decay, out, den=None, normalize=True, eps=1e-6,
+                        lengths=None, S_in=None, z_in=None, S_out=None, z_out=None,
+                        workspace=None, stream=None):
+    """Causal linear attention on given features phq, phk [B,H,L,F] whose weights decay by
+    exp(log_decay[h]) a token, from state (S_in, z_in) (None: zero) to (S_out, z_out) if given;
+    lengths [B] int32: the tokens of each sequence of a padded batch.  Returns the workspace."""
+    dev, B, H, L, F, Dv = _decay_common(phq, phk, v, log_decay, lengths)
+    _check_on(dev, out, "out", phq.dtype, (B, H, L, Dv))
+    _check_on(dev, den, "den", torch.float32, (B, H, L), optional=True)
+    _decay_pair(dev, S_in, z_in, (B, H, F), normalize, "in")
+    _decay_pair(dev, S_out, z_out, (B, H, F), normalize, "out")
+    dt = _dt(phq)
+    with torch.cuda.device(dev):
+        workspace, wbytes = _decay_workspace(OP_DECAY_FWD, dt, B, H, L, F, Dv, workspace, dev)
+        _raise(lib().slay_decay_attn_fwd(
+            _ptr(phq), _ptr(phk), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(S_in), _ptr(z_in),
+            _ptr(out), _ptr(den), _ptr(S_out), _ptr(z_out), B, H, L, F, Dv, dt, int(bool(normalize)),
+            eps, _ptr(workspace), wbytes, _stream_on(dev, stream)), "slay_decay_attn_fwd")
+    return workspace
+
+
+def slay_decay_attn_bwd(phq, phk, v, log_decay, dout, dphq, dphk, dv, out=None, den=None,
+                        normalize=True, eps=1e-6, lengths=None, S_in=None, z_in=None, dS_out=None,
+                        dz_out=None, dS_in=None, dz_in=None, workspace=None, stream=None):
+    """Gradients of slay_decay_attn_fwd, in the inputs' dtype (out, den: the forward's, needed
+    when normalized; dS_out, dz_out: gradients of the final state; dS_in, dz_in: of the first).
+    Returns the workspace."""
+    dev, B, H, L, F, Dv = _decay_common(phq, phk, v, log_decay, lengths)
+    _check_on(dev, dout, "dout", phq.dtype, (B, H, L, Dv))
+    _check_on(dev, out, "out", phq.dtype, (B, H, L, Dv), optional=not normalize)
+    _check_on(dev, den, "den", torch.float32, (B, H, L), optional=not normalize)
+    _check_on(dev, dphq, "dphq", phq.dtype, (B, H, L, F))
+    _check_on(dev, dphk, "dphk", phq.dtype, (B, H, L, F))
+    _check_on(dev, dv, "dv", phq.dtype, (B, H, L, Dv))
+    _decay_pair(dev, S_in, z_in, (B, H, F), normalize, "in")
+    _decay_pair(dev, dS_out, dz_out, (B, H, F), normalize, "out gradient")
+    _decay_pair(dev, dS_in, dz_in, (B, H, F), normalize, "in gradient")
+    dt = _dt(phq)
+    with torch.cuda.device(dev):
+        workspace, wbytes = _decay_workspace(OP_DECAY_BWD, dt, B, H, L, F, Dv, workspace, dev)
+        _raise(lib().slay_decay_attn_bwd(
+            _ptr(phq), _ptr(phk), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(S_in), _ptr(z_in),
+            _ptr(out), _ptr(den), _ptr(dout), _ptr(dS_out), _ptr(dz_out), _ptr(dphq), _ptr(dphk),
+            _ptr(dv), _ptr(dS_in), _ptr(dz_in), B, H, L, F, Dv, dt, int(bool(normalize)), eps,
+            _ptr(workspace), wbytes, _stream_on(dev, stream)), "slay_decay_attn_bwd")
+    return workspace
+
+
+def slay_decay_decode_step(phq, phk, v, log_decay, S, z, out, slots=None, normalize=True,
+                           eps=1e-6, stream=None):
+    """One decayed step of each batch row b (phq, phk [Bt,H,F], v, out [Bt,H,64]) on the pool
+    slot slots[b] (None: slot b) of S [n,H,F,64], z [n,H,F] (None when not normalized), in
+    place; rows with a slot outside the pool, such as -1, are left out."""
+    _check(phq, "phq")
+    if phq.dim() != 3 or v is None or v.dim() != 3 or S is None or S.dim() != 4:
+        raise ValueError("phq, phk are [Bt, H, F], v is [Bt, H, Dv] and S [n, H, F, Dv]")
+    Bt, H, F = phq.shape
+    dev, Dv, n = phq.device, v.shape[-1], S.shape[0]
+    _check_on(dev, phk, "phk", phq.dtype, (Bt, H, F))
+    _check_on(dev, v, "v", phq.dtype, (Bt, H, Dv))
+    _check_on(dev, out, "out", phq.dtype, (Bt, H, Dv))
+    _check_on(dev, log_decay, "log_decay", torch.float32, (H,))
+    _check_on(dev, slots, "slots", torch.int32, (Bt,), optional=True)
+    _decay_pair(dev, S, z, (n, H, F), normalize, "pool")
+    if slots is None and Bt > n:
+        raise ValueError("%d rows, but the pool has %d slots" % (Bt, n))
+    with torch.cuda.device(dev):
+        _raise(lib().slay_decay_decode_step(
+            _ptr(phq), _ptr(phk), _ptr(v), _ptr(log_decay), _ptr(S), _ptr(z), _ptr(slots), _ptr(out),
+            Bt, H, F, Dv, n, _dt(phq), int(bool(normalize)), eps, _stream_on(dev, stream)),
+            "slay_decay_decode_step")
+
+
+def slay_state_copy(S_src, z_src, src, S_dst, z_dst, dst, stream=None):
+    """Slot dst[i] of (S_dst, z_dst) becomes slot src[i] of (S_src, z_src), or zero where src[i]
+    is -1, every source read as it was before the call (one pool may be given as both)."""
+    _check(S_src, "S_src", torch.float32)
+    if S_src.dim() != 4 or S_dst is None or S_dst.dim() != 4 or src is None:
+        raise ValueError("pools are [n, H, F, Dv]; src and dst are [n]")
+    n_src, H, F, Dv = S_src.shape
+    dev, n_dst = S_src.device, S_dst.shape[0]
+    _check_on(dev, S_dst, "S_dst", torch.float32, (n_dst, H, F, Dv))
+    if (z_src is None) != (z_dst is None):
+        raise ValueError("z_src and z_dst go together")
+    _check_on(dev, z_src, "z_src", torch.float32, (n_src, H, F), optional=True)
+    _check_on(dev, z_dst, "z_dst", torch.float32, (n_dst, H, F), optional=True)
+    _check_on(dev, src, "src", torch.int32, (src.numel(),))
+    _check_on(dev, dst, "dst", torch.int32, (src.numel(),))
+    with torch.cuda.device(dev):
+        _raise(lib().slay_state_copy(
+            _ptr(S_src), _ptr(z_src), _ptr(src), n_src, _ptr(S_dst), _ptr(z_dst), _ptr(dst), n_dst,
+            src.numel(), H, F, Dv, _stream_on(dev, stream)), "slay_state_copy")

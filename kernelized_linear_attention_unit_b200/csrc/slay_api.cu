@@ -202,6 +202,7 @@ slay_status get_var_params(int D, int R, int m, uint64_t seed, float eps, int ki
 
 }  // namespace
 
+slay_status report_cuda(cudaError_t e) { return cuda_fail(e); }
 bool eps_ok(float eps) { return std::isfinite(eps) && eps > 0.0f; }
 bool dtype_ok(slay_dtype d) { return d == SLAY_F32 || d == SLAY_BF16; }
 
@@ -789,6 +790,7 @@ size_t slay_workspace_bytes(slay_op op, slay_dtype dt, int B, int H, int L, int 
     if (check_shape(D, Dv, R, m) != SLAY_OK) return SIZE_MAX;
     if (op == SLAY_OP_FEATURE_MAP || op == SLAY_OP_DECODE || op == SLAY_OP_FEATURE_MAP_BWD)
         return 0;
+    if (op == SLAY_OP_DECAY_FWD || op == SLAY_OP_DECAY_BWD) return decay_ws(op, dt, B, H, L, R * m);
     if (op != SLAY_OP_CAUSAL_FWD && op != SLAY_OP_BIDIR_FWD && op != SLAY_OP_CAUSAL_BWD &&
         op != SLAY_OP_BIDIR_BWD && op != SLAY_OP_LINEAR_ATTN && op != SLAY_OP_CAUSAL_STATE &&
         op != SLAY_OP_CAUSAL_FWD_SPLIT)
@@ -807,6 +809,10 @@ int slay_path(slay_op op, slay_dtype dt, int B, int H, int L, int D, int Dv, int
     if (op == SLAY_OP_LINEAR_ATTN) {   // R * m features given; the chunk kernels on CUDA cores
         if (R <= 0 || m <= 0 || Dv != kD || static_cast<int64_t>(R) * m > kMaxF) return -1;
         return 0;
+    }
+    if (op == SLAY_OP_DECAY_FWD || op == SLAY_OP_DECAY_BWD) {   // R * m features given
+        if (check_shape(kD, Dv, R, m) != SLAY_OK) return -1;
+        return decay_path(op, dt, B, H, L, R * m);
     }
     if (check_shape(D, Dv, R, m) != SLAY_OK) return -1;
     const bool bf = dt == SLAY_BF16;

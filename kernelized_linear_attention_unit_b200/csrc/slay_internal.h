@@ -79,10 +79,15 @@ slay_status check_attn(const void* q, const void* k, const void* v, const void* 
 // kernel status word: 0 after a call is enqueued, set to 1 by a kernel whose bounded
 // mbarrier wait ran out.  The path's own scratch follows the header.
 constexpr size_t kWsHeader = 256;
+// Keep a CUDA error's text for slay_last_error; returns SLAY_ERR_CUDA.
+slay_status report_cuda(cudaError_t e);
 size_t attn_ws(slay_op op, slay_dtype dt, int B, int H, int L, int Dv, int R, int m);
 // Device address of the no-alloc path's status word on the current device, or nullptr
 // when that path has not run on it.
 const void* noalloc_status_word();
+// Workspace bytes and slay_path mask of the decayed forward and backward (slay_decay_api.cu).
+size_t decay_ws(slay_op op, slay_dtype dt, int B, int H, int L, int F);
+int decay_path(slay_op op, slay_dtype dt, int B, int H, int L, int F);
 
 // ---- CUDA-core kernels (slay_simt.cu) ----
 // Sizes of the workspace carve-outs of the CUDA-core path.

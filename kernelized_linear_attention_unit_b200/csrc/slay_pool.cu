@@ -1,0 +1,268 @@
+// slay_pool.cu -- states of running sequences in the slots of a pool: one decayed decode step
+// on the slots a batch names, and copies between slots (fork, move, clear).
+//
+// Both move each state once each way and compute next to nothing, so HBM bounds them:
+// 8 F 65 bytes per head and step, 4 F 65 bytes read and written per head and copied slot.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "slay_decay.h"
+
+namespace slay {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kNT = 256;
+constexpr int kNumSMs = 148;
+
+__device__ __forceinline__ float ldf(const float* p) { return *p; }
+__device__ __forceinline__ float ldf(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void stf(float* p, float x) { *p = x; }
+__device__ __forceinline__ void stf(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// ------------------------------------------------------------------------ decode
+// S <- lambda S + k v^T, z <- lambda z + k, out = q^T S (/ (q . z + eps)) for batch row b and
+// head h on slot slots[b].  A cluster of CTAs shares one (b, h), each a contiguous share of
+// the F rows of S; 16 threads cover a row's 64 columns, and the partial numerators and
+// denominators join in the first CTA through distributed shared memory.
+// A row whose slot is outside the pool, or was already named by an earlier row, is left out:
+// its out row and the slot stay as they were (two rows must not step one state at once).
+template <typename T>
+__global__ void __launch_bounds__(kNT) k_decay_decode(const T* __restrict__ phq, const T* __restrict__ phk,
+                                                      const T* __restrict__ v, const float* __restrict__ log_decay,
+                                                      float* __restrict__ S, float* __restrict__ z,
+                                                      const int32_t* __restrict__ slots, T* __restrict__ out, int H,
+                                                      int F, int n_slots, int norm, float eps)
+{
+    extern __shared__ __align__(16) float sm[];   // q and k of this CTA's features
+    __shared__ float red[16][64];
+    __shared__ float part[65];
+    __shared__ float dred[kNT / 32];
+    cg::cluster_group cl = cg::this_cluster();
+    const int cs = cl.num_blocks(), rank = cl.block_rank();
+    const int64_t bh = blockIdx.x / cs;
+    const int b = static_cast<int>(bh / H), h = static_cast<int>(bh % H), tid = threadIdx.x;
+    const int slot = slots ? slots[b] : b;
+    int skip = slot < 0 || slot >= n_slots;
+    if (slots)
+        for (int i = tid; i < b; i += kNT) skip |= slots[i] == slot;
+    if (__syncthreads_or(skip)) return;           // the whole cluster sees the same answer
+    const int share = (F + cs - 1) / cs, f0 = min(rank * share, F), n = min(share, F - f0);
+    float* qs = sm;
+    float* ks = sm + share;
+    for (int f = tid; f < n; f += kNT) {
+        qs[f] = ldf(phq + bh * F + f0 + f);
+        ks[f] = ldf(phk + bh * F + f0 + f);
+    }
+    const float lam = expf(log_decay[h]);
+    const int e4 = (tid & 15) * 4, fr = tid >> 4;
+    const T* vp = v + bh * 64 + e4;
+    const float4 vv = make_float4(ldf(vp), ldf(vp + 1), ldf(vp + 2), ldf(vp + 3));
+    __syncthreads();
+    const int64_t sh = static_cast<int64_t>(slot) * H + h;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4* Sp = reinterpret_cast<float4*>(S + (sh * F + f0) * 64 + e4);
+#pragma unroll 8
+    for (int f = fr; f < n; f += 16) {
+        float4 s = Sp[f * 16];
+        const float a = ks[f], c = qs[f];
+        s.x = fmaf(lam, s.x, a * vv.x);
+        s.y = fmaf(lam, s.y, a * vv.y);
+        s.z = fmaf(lam, s.z, a * vv.z);
+        s.w = fmaf(lam, s.w, a * vv.w);
+        Sp[f * 16] = s;
+        acc.x = fmaf(c, s.x, acc.x);
+        acc.y = fmaf(c, s.y, acc.y);
+        acc.z = fmaf(c, s.z, acc.z);
+        acc.w = fmaf(c, s.w, acc.w);
+    }
+    *reinterpret_cast<float4*>(&red[fr][e4]) = acc;
+    if (norm) {
+        float d = 0.0f;
+        float* zp = z + sh * F + f0;
+        for (int f = tid; f < n; f += kNT) {
+            const float w = fmaf(lam, zp[f], ks[f]);
+            zp[f] = w;
+            d = fmaf(qs[f], w, d);
+        }
+        for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
+        if ((tid & 31) == 0) dred[tid >> 5] = d;
+    }
+    __syncthreads();
+    if (tid < 64) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s += red[i][tid];
+        part[tid] = s;
+    } else if (tid == 64) {
+        float d = 0.0f;
+        for (int i = 0; i < kNT / 32; ++i) d += norm ? dred[i] : 0.0f;
+        part[64] = d;
+    }
+    cl.sync();
+    if (rank == 0 && tid < 64) {
+        float s = 0.0f, d = 0.0f;
+        for (int i = 0; i < cs; ++i) {
+            const float* p = cl.map_shared_rank(part, i);
+            s += p[tid];
+            d += p[64];
+        }
+        stf(out + bh * 64 + tid, norm ? s / (d + eps) : s);
+    }
+    cl.sync();   // the peers' shared memory stays until it has been read
+}
+
+template <typename T>
+cudaError_t decode_t(const DecodeArgs& a, cudaStream_t st)
+{
+    // one CTA per (row, head) when those fill the GPU twice over, else up to 8 that share it
+    // (at least 16 features each: one pass of the CTA)
+    const int64_t bh = static_cast<int64_t>(a.B) * a.H;
+    int cs = 1;
+    while (cs < 8 && bh * cs < 2 * kNumSMs && a.F >= 32 * cs) cs *= 2;
+    const size_t smem = 2 * static_cast<size_t>((a.F + cs - 1) / cs) * sizeof(float);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(bh * cs));
+    cfg.blockDim = dim3(kNT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cs;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    TraceScope trace_("decay_decode", st);
+    return cudaLaunchKernelEx(&cfg, k_decay_decode<T>, static_cast<const T*>(a.phq), static_cast<const T*>(a.phk),
+                              static_cast<const T*>(a.v), a.log_decay, a.S, a.z, a.slots, static_cast<T*>(a.out), a.H,
+                              a.F, a.n_slots, a.norm ? 1 : 0, a.eps);
+}
+
+// ------------------------------------------------------------------------- copies
+// dst[i] <- src[i] for n pairs of slots, every source read as it was before the call.  A CTA
+// owns a range of columns (`width` bytes of every slot): it reads its columns of all sources
+// into shared memory, then writes them to the destinations, so a slot may be both a source
+// and a destination, in any cycle, with no order between CTAs.  Where a destination is named
+// more than once the last pair wins: a hash table in shared memory keeps, per destination,
+// the highest pair index.
+template <typename U>
+__device__ __forceinline__ void copy_columns(const U* src_base, U* dst_base, int64_t slot_units, int64_t c0, int wu,
+                                             int n, const int* src, const int* dst, U* stage)
+{
+    // wu units (a power of two) of each of n slots, columns [c0, c0 + wu) cut at slot_units
+    for (int i = threadIdx.x; i < n * wu; i += kNT) {
+        const int p = i / wu, c = i & (wu - 1);
+        if (dst[p] < 0 || c0 + c >= slot_units) continue;
+        if (src[p] >= 0) {
+            const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(stage + i));
+            const U* g = src_base + src[p] * slot_units + c0 + c;
+            if (sizeof(U) == 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(g) : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s), "l"(g) : "memory");
+        } else {
+            stage[i] = U{};
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    for (int i = threadIdx.x; i < n * wu; i += kNT) {
+        const int p = i / wu, c = i & (wu - 1);
+        if (dst[p] < 0 || c0 + c >= slot_units) continue;
+        dst_base[dst[p] * slot_units + c0 + c] = stage[i];
+    }
+    __syncthreads();   // the stage is free again
+}
+
+__global__ void __launch_bounds__(kNT) k_state_copy(CopyArgs a, int wS, int nS, int wZ, int nZ, int z16, int table)
+{
+    extern __shared__ __align__(16) unsigned char raw[];
+    int* src = reinterpret_cast<int*>(raw);
+    int* dst = src + ((a.n + 3) & ~3);
+    int* key = dst + ((a.n + 3) & ~3);   // [table], then the highest pair index [table]
+    int* top = key + table;
+    unsigned char* stage = reinterpret_cast<unsigned char*>(dst + ((a.n + 3) & ~3));   // after the table's use
+    const int tid = threadIdx.x;
+    for (int i = tid; i < table; i += kNT) { key[i] = -1; top[i] = -1; }
+    __syncthreads();
+    for (int i = tid; i < a.n; i += kNT) {
+        const int s = a.src[i], d = a.dst[i];
+        const bool ok = d >= 0 && d < a.n_dst && s >= -1 && s < a.n_src;
+        src[i] = s;
+        dst[i] = ok ? d : -1;
+        if (!ok) continue;
+        uint32_t at = (static_cast<uint32_t>(d) * 2654435761u) & (table - 1);
+        for (int probe = 0; probe < table; ++probe) {
+            const int was = atomicCAS(&key[at], -1, d);
+            if (was == -1 || was == d) { atomicMax(&top[at], i); break; }
+            at = (at + 1) & (table - 1);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < a.n; i += kNT) {
+        const int d = dst[i];
+        if (d < 0) continue;
+        uint32_t at = (static_cast<uint32_t>(d) * 2654435761u) & (table - 1);
+        for (int probe = 0; probe < table && key[at] != d; ++probe) at = (at + 1) & (table - 1);
+        if (top[at] != i) dst[i] = -1;   // a later pair writes this destination
+    }
+    __syncthreads();
+    for (int w = blockIdx.x; w < nS + nZ; w += gridDim.x) {
+        if (w < nS)
+            copy_columns(reinterpret_cast<const float4*>(a.S_src), reinterpret_cast<float4*>(a.S_dst), a.hf * 16,
+                         static_cast<int64_t>(w) * wS, wS, a.n, src, dst, reinterpret_cast<float4*>(stage));
+        else if (z16)
+            copy_columns(reinterpret_cast<const float4*>(a.z_src), reinterpret_cast<float4*>(a.z_dst), a.hf / 4,
+                         static_cast<int64_t>(w - nS) * wZ, wZ, a.n, src, dst, reinterpret_cast<float4*>(stage));
+        else
+            copy_columns(a.z_src, a.z_dst, a.hf, static_cast<int64_t>(w - nS) * wZ, wZ, a.n, src, dst,
+                         reinterpret_cast<float*>(stage));
+    }
+}
+
+}  // namespace
+
+cudaError_t decay_decode(const DecodeArgs& a, cudaStream_t st)
+{
+    return a.dt == SLAY_F32 ? decode_t<float>(a, st) : decode_t<__nv_bfloat16>(a, st);
+}
+
+cudaError_t state_copy(const CopyArgs& a, cudaStream_t st)
+{
+    int table = 32;
+    while (table < 2 * a.n) table *= 2;
+    const size_t lists = 2 * static_cast<size_t>((a.n + 3) & ~3) * sizeof(int);
+    // column width in 16-byte units: the widest power of two, at most 64 (1 KiB), whose
+    // stage leaves room for two CTAs on an SM and that gives every SM two ranges of columns
+    const size_t budget = 100 * 1024 - lists;
+    auto width = [&](int64_t units, size_t unit) {
+        int w = 64;
+        while (w > 1 && (static_cast<size_t>(a.n) * w * unit > budget || (units + w - 1) / w < 2 * kNumSMs)) w /= 2;
+        return w;
+    };
+    const int64_t uS = a.hf * 16;
+    const int wS = width(uS, 16);
+    const int nS = static_cast<int>((uS + wS - 1) / wS);
+    const int z16 = a.z_src && a.hf % 4 == 0;
+    const int64_t uZ = a.z_src ? (z16 ? a.hf / 4 : a.hf) : 0;
+    const int wZ = width(uZ, 16);
+    const int nZ = static_cast<int>((uZ + wZ - 1) / wZ);
+    const size_t stage = static_cast<size_t>(a.n) * std::max(wS, wZ) * 16;
+    const size_t smem = lists + std::max(stage, 2 * static_cast<size_t>(table) * sizeof(int));
+    cudaError_t e = cudaFuncSetAttribute(k_state_copy, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    int per_sm = 1;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_state_copy, kNT, smem);
+    if (e != cudaSuccess) return e;
+    const int grid = std::min(nS + nZ, std::max(1, per_sm) * kNumSMs);
+    TraceScope trace_("state_copy", st);
+    k_state_copy<<<grid, kNT, smem, st>>>(a, wS, nS, wZ, nZ, z16, table);
+    return cudaGetLastError();
+}
+
+}  // namespace slay
