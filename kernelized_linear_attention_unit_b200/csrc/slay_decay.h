@@ -69,6 +69,13 @@ size_t decay_simt_ws(const DecayArgs& a, bool bwd);
 cudaError_t decay_simt_fwd(const DecayArgs& a, void* ws, cudaStream_t st);
 cudaError_t decay_simt_bwd(const DecayArgs& a, void* ws, cudaStream_t st);
 
+// Tensor cores: bf16, F % 8 == 0, F <= 512 (feature blocks of at most 256).  err: the status
+// word a bounded wait that ran out is reported in.
+bool decay_tc_supported(const DecayArgs& a);
+size_t decay_tc_ws(const DecayArgs& a, bool bwd);
+cudaError_t decay_tc_fwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st);
+cudaError_t decay_tc_bwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st);
+
 // Single-token step on pooled states; pool copies.
 struct DecodeArgs {
     const void *phq, *phk, *v;

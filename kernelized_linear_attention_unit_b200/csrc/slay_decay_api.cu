@@ -55,10 +55,13 @@ size_t decay_ws(slay_op op, slay_dtype dt, int B, int H, int L, int F)
     if (static_cast<int64_t>(B) * H * L == 0) return 0;
     const DecayArgs a = sizes(B, H, L, F, dt, true);
     const bool bwd = op == SLAY_OP_DECAY_BWD;
-    return kWsHeader + decay_simt_ws(a, bwd);
+    return kWsHeader + (decay_tc_supported(a) ? decay_tc_ws(a, bwd) : decay_simt_ws(a, bwd));
 }
 
-int decay_path(slay_op, slay_dtype, int, int, int, int) { return 0; }
+int decay_path(slay_op, slay_dtype dt, int B, int H, int L, int F)
+{
+    return static_cast<int64_t>(B) * H > 0 && decay_tc_supported(sizes(B, H, L, F, dt, true)) ? SLAY_PATH_TC_CONTRACTION : 0;
+}
 
 }  // namespace slay
 
@@ -97,7 +100,9 @@ slay_status slay_decay_attn_fwd(const void* phq, const void* phk, const void* v,
     a.z_out = z_out;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = need ? cudaMemsetAsync(workspace, 0, sizeof(int), st) : cudaSuccess;
-    if (e == cudaSuccess) e = decay_simt_fwd(a, static_cast<char*>(workspace) + kWsHeader, st);
+    void* scratch = static_cast<char*>(workspace) + kWsHeader;
+    if (e == cudaSuccess)
+        e = decay_tc_supported(a) ? decay_tc_fwd(a, scratch, static_cast<int*>(workspace), st) : decay_simt_fwd(a, scratch, st);
     return e == cudaSuccess ? SLAY_OK : report_cuda(e);
 }
 
@@ -143,7 +148,9 @@ slay_status slay_decay_attn_bwd(const void* phq, const void* phk, const void* v,
     a.dz_in = dz_in;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = need ? cudaMemsetAsync(workspace, 0, sizeof(int), st) : cudaSuccess;
-    if (e == cudaSuccess) e = decay_simt_bwd(a, static_cast<char*>(workspace) + kWsHeader, st);
+    void* scratch = static_cast<char*>(workspace) + kWsHeader;
+    if (e == cudaSuccess)
+        e = decay_tc_supported(a) ? decay_tc_bwd(a, scratch, static_cast<int*>(workspace), st) : decay_simt_bwd(a, scratch, st);
     return e == cudaSuccess ? SLAY_OK : report_cuda(e);
 }
 
