@@ -44,23 +44,29 @@ constexpr int kT = 128;               // tokens per chunk
 constexpr int kTile = kT * 128;       // [128][64] bf16, 128-byte swizzle = 16 KiB
 constexpr int kSlab = 64 * 128;       // [64 f][64 e] bf16 = 8 KiB
 constexpr int kExt = 16 * 128;        // [16][64] bf16 = 2 KiB
-constexpr int kThreads = 32 * 10;     // MMA warp, TMA warp, 8 epilogue warps
+constexpr int kThreads = 32 * 12;     // MMA warp, TMA warp (and two idle ones), 8 epilogue warps
 constexpr int kNumSMs = 148;
 constexpr int kMaxFw = 256;           // features of one sweep
 
 enum Mode { kState = 0, kOutF = 1, kOutE = 2 };
 
-// tensor memory columns
-constexpr uint32_t kColP = 0, kColPt = 128, kColT = 192, kColO = 352;
-constexpr uint32_t kTStride = 80;     // T of 128 features: 64 columns and 16 for z
+// tensor memory columns.  P~ replaces the scores' first 64 columns; an output accumulator
+// takes the other 64.  T of 128 features: the first limb's 64 columns, in the modes with
+// room a second limb's, and 16 for z.
+constexpr uint32_t kColP = 0, kColOi = 64, kColOe = 128, kColDen = 192;
+constexpr uint32_t kColOi0 = 128, kColOe0 = 192, kColOe1 = 256;   // kOutE: buffer 0; buffer 1 is kColOi, kColOe1
+__host__ __device__ constexpr uint32_t col_t(int mode) { return mode == kOutE ? 352 : 208; }
+__host__ __device__ constexpr uint32_t col_z(int mode) { return mode == kOutE ? 64 : 128; }
+__host__ __device__ constexpr uint32_t t_stride(int mode) { return mode == kOutE ? 80 : 144; }
+__host__ __device__ constexpr int limb_tiles(int mode) { return mode == kState ? 6 : mode == kOutE ? 2 : 3; }
 
 enum {
-    B_FSF = 0, B_FSE = 4, B_FQF = 8, B_FQE = 10, B_ESF = 12, B_ESE = 14, B_YF = 16, B_MF, B_PF, B_PT, B_TF,
-    B_OF = 21, B_OE = 23, B_NUM = 25
+    B_FSF = 0, B_FSE = 4, B_FQF = 8, B_FQE = 10, B_ESF = 12, B_ESE = 14, B_YF = 16, B_MF = 18, B_PF, B_PT, B_TF, B_OD,
+    B_OF = 23, B_OE = 25, B_NUM = 27
 };
 
 struct Layout {
-    uint32_t fs, fq, es, eq, y, m, zext, wext, pw, smul, soff, dsum, zf, bar, tmem, total;
+    uint32_t fs, fq, es, eq, y, m, zext, wext, stg, pw, smul, soff, dsum, zf, bar, tmem, total;
 };
 
 __host__ __device__ constexpr Layout layout(int mode)
@@ -71,15 +77,16 @@ __host__ __device__ constexpr Layout layout(int mode)
     l.fq = o; o += mode == kOutF ? 2 * kTile : 0;       // ring of two query slices
     l.es = o; o += 2 * kTile;                           // 64-wide side, two chunks
     l.eq = o; o += mode == kOutE ? 2 * kTile : 0;       // 64-wide queries, two chunks
-    l.y = o; o += 3 * kTile;                            // weighted rows, three limbs
+    l.y = o; o += limb_tiles(mode) * kTile;             // weighted rows in limbs (kState: two chunks)
     l.m = o; o += mode == kState ? 0 : 4 * kSlab;       // the state as an operand
     l.zext = o; o += mode == kOutF ? 4 * kExt : 0;      // its z column, three limbs of 16 columns
-    l.wext = o; o += 2 * kExt;                          // z weights of the chunk's tokens, likewise
+    l.wext = o; o += (mode == kState ? 4 : 2) * kExt;   // z weights of the chunk's tokens, likewise
+    l.stg = o; o += mode == kOutE ? 8 * 32 * 64 : 0;    // outputs on their way to the TMA store, 2 KiB a warp
     l.pw = o; o += 128 * 4;                             // lambda^d
     l.smul = o; o += 2 * 128 * 4;                       // score scalars of the state tokens
     l.soff = o; o += 2 * 128 * 4;
-    l.dsum = o; o += mode == kOutF ? 2 * 2 * 128 * 4 : 0;                   // row sums of the scores, by column half
-    l.zf = o; o += mode == kOutE ? 2 * kMaxFw * 4 : 0;                      // z in fp32
+    l.dsum = o; o += mode == kOutF ? 2 * 2 * 128 * 4 : 0;   // row sums of the scores, by column half
+    l.zf = o; o += mode == kOutE ? 2 * kMaxFw * 4 : 0;  // z in fp32, two chunks
     l.bar = o; o += B_NUM * 8;
     l.tmem = o; o += 16;
     l.total = o;
@@ -98,7 +105,7 @@ struct P {
     int part_mode;                                // 0: none, 1: store them, 2: add them to this block's
     float eps;
     int H, L, F, nseg, nfb, fw, fb0;
-    int rev, has_z, z_delta, has_den;
+    int z_state;                                  // keep z (kOutF backward: only where it is wanted)
     int* err;
 };
 
@@ -116,18 +123,52 @@ __device__ __forceinline__ void limbs3(float x, uint16_t (&l)[3])
     }
 }
 
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) { return ffma2(a, make_float2(1.0f, 1.0f), b); }
+
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t x)
 {
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(x) : "memory");
 }
 
-template <int kMode>
+// A wait on the completion of `phase`, bounded by a number of tries (each suspends the thread
+// for a time that the hardware chooses): between about 0.05 s and a few seconds.
+struct Bounded {
+    bool ok = true;
+    uint32_t where = 0;
+    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase)
+    {
+        const uint32_t addr = smem_u32(bar);
+        if (mbar_try_wait(addr, phase)) return;
+        for (int it = ok ? 1 << 22 : 1; it > 0; --it)
+            if (mbar_try_wait(addr, phase)) return;
+        if (ok) where = 0x10000u | (addr & 0xFFFFu);
+        ok = false;
+    }
+    __device__ __forceinline__ void report(int* status) const
+    {
+        if (!ok) atomicCAS(status, 0, static_cast<int>(where));
+    }
+};
+
+// One lane of a converged warp; the compiler knows that a single thread runs what it guards.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// kRev: the sweep walks the chunks backward.  kNorm: the normalized form, whose backward puts
+// its row scalars on the state tokens (kRev) or on the query tokens (kOutE forward).
+template <int kMode, bool kRev, bool kNorm>
 __global__ void __launch_bounds__(kThreads, 1)
 k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtensorMap tfq,
-         const __grid_constant__ CUtensorMap tes, const __grid_constant__ CUtensorMap teq, const P p)
+         const __grid_constant__ CUtensorMap tes, const __grid_constant__ CUtensorMap teq,
+         const __grid_constant__ CUtensorMap tout, const P p)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char* sm = aligned_smem(smem_raw);
+    unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // (stays a shared address)
+    constexpr bool kCols = kRev && kNorm, kRows = kMode == kOutE && !kRev && kNorm, kDen = kMode == kOutF && !kRev && kNorm;
     constexpr Layout Lo = layout(kMode);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Lo.bar);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Lo.tmem);
@@ -143,22 +184,27 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     const int ns = (fv + 63) >> 6, nsE = (ns + 1) & ~1;   // 64-feature slices; as whole pairs
     const int len = p.lengths ? min(max(p.lengths[bh / p.H], 0), p.L) : p.L;
     const int nch = (len + kT - 1) / kT;
-    const int c_lo = static_cast<int>(static_cast<int64_t>(seg) * nch / p.nseg);
-    const int count = static_cast<int>(static_cast<int64_t>(seg + 1) * nch / p.nseg) - c_lo;
-    auto chunk_of = [&](int i) { return p.rev ? c_lo + count - 1 - i : c_lo + i; };
+    const int c_lo = seg * nch / p.nseg;                  // (at most 32768 chunks, 148 segments)
+    const int count = (seg + 1) * nch / p.nseg - c_lo;
+    auto chunk_of = [&](int i) { return kRev ? c_lo + count - 1 - i : c_lo + i; };
     const float g2 = p.log_decay[bh % p.H] * kLog2e;
-    // without decay and row scalars the weights are 1 and one limb is exact
-    const int nl = g2 == 0.0f && !p.s_mul ? 1 : 3;
+    // limbs of the weighted rows: three where the fp32 state leaves the call, two (2^-17) where
+    // only its bf16 copy is read; without decay and row scalars the weights are 1, one is exact
+    const bool has_z = kNorm && (kMode != kOutF || !kRev || p.z_state);
+    const int nl = g2 == 0.0f && !kCols ? 1 : (kMode == kState || (kMode == kOutF && p.last)) ? 3 : 2;
 
     if (warp == 0) {
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
-    for (uint32_t i = Lo.zext / 4 + tid; i < Lo.pw / 4; i += kThreads) reinterpret_cast<uint32_t*>(sm)[i] = 0u;
-    if (tid < kT) reinterpret_cast<float*>(sm + Lo.pw)[tid] = decay_pow(g2, tid);
+    for (uint32_t i = Lo.zext / 4 + tid; i < Lo.stg / 4; i += kThreads) reinterpret_cast<uint32_t*>(sm)[i] = 0u;
+    // lambda powers: within a diagonal block of scores, at 31 + distance (zero where it is masked),
+    // then the column factors of a block inside the mask
+    if (tid < 64) reinterpret_cast<float*>(sm + Lo.pw)[tid] = tid >= 31 && tid < 63 ? decay_pow(g2, tid - 31) : 0.0f;
+    if (tid < 32) reinterpret_cast<float*>(sm + Lo.pw)[64 + tid] = decay_pow(g2, kRev ? tid : 31 - tid);
     if (tid == 0) {
         for (int i = 0; i < B_NUM; ++i)
-            mbar_init(&bar[i], i == B_YF || i == B_MF || i == B_PT || i == B_OE || i == B_OE + 1 ? 8 : 1);
+            mbar_init(&bar[i], i == B_YF || i == B_YF + 1 || i == B_MF || i == B_PT || i == B_OE || i == B_OE + 1 ? 8 : 1);
         mbar_fence_init();
         tma_prefetch_desc(&tfs);
         tma_prefetch_desc(&tes);
@@ -169,17 +215,21 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tslot;
-    Waiter wt;
+    constexpr uint32_t tmem = 0;   // all 512 columns are this CTA's
+    Bounded wt;
+    if (*tslot != tmem) {
+        wt.ok = false;
+        wt.where = 0x20000u;
+    }
     // waits on the k-th completion (k >= 0) of a barrier
-    auto wait_k = [&](int b, int k) {
-        uint32_t ph = static_cast<uint32_t>(k & 1);
-        wt.wait(&bar[b], ph);
-    };
+    auto wait_k = [&](int b, int k) { wt.wait(&bar[b], static_cast<uint32_t>(k & 1)); };
 
-    if (warp == 1) {
-        // ------------------------------------------------------------------ TMA loads
-        if (lane == 0) {
+    // Registers: 384 threads launch with 168 each; the loading warpgroup gives some of its share
+    // to the epilogue, which holds the state: 88 + 2 x 208 = 3 x 168.
+    if (warp < 4) {
+        regs_dec<88>();
+        if (warp == 1 && lane == 0) {
+            // -------------------------------------------------------------- TMA loads
             for (int i = 0; i < count && wt.ok; ++i) {
                 const int t0 = chunk_of(i) * kT, b = i & 1;
                 if (i >= 2) wait_k(B_ESE + b, (i >> 1) - 1);
@@ -203,152 +253,180 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                     }
                 }
             }
-        }
-        __syncwarp();
-    } else if (warp == 0) {
-        // ------------------------------------------------------------------ MMA issue
-        constexpr uint32_t idP = idesc_bf16(128, 128, 0, 0);
-        constexpr uint32_t idKM = idesc_bf16(128, 64, 0, 1);    // A K-major (or tensor memory), B MN-major
-        constexpr uint32_t idKK = idesc_bf16(128, 64, 0, 0);
-        constexpr uint32_t idMM = idesc_bf16(128, 64, 1, 1);
-        constexpr uint32_t idMz = idesc_bf16(128, 16, 1, 0);
-        constexpr uint32_t idKz = idesc_bf16(128, 16, 0, 0);
-        const uint64_t dfs = sdesc(sbase + Lo.fs, 16, 1024, kLayoutSW128);
-        const uint64_t dfsT = sdesc(sbase + Lo.fs, kTile, 1024, kLayoutSW128);   // M = 128 over two slices
-        const uint64_t dfq = sdesc(sbase + Lo.fq, 16, 1024, kLayoutSW128);
-        const uint64_t des = sdesc(sbase + Lo.es, 16, 1024, kLayoutSW128);
-        const uint64_t deq = sdesc(sbase + Lo.eq, 16, 1024, kLayoutSW128);
-        const uint64_t dy = sdesc(sbase + Lo.y, 16, 1024, kLayoutSW128);
-        const uint64_t dm = sdesc(sbase + Lo.m, 16, 1024, kLayoutSW128);
-        const uint64_t dze = sdesc(sbase + Lo.zext, 16, 1024, kLayoutSW128);
-        const uint64_t dwe = sdesc(sbase + Lo.wext, 16, 1024, kLayoutSW128);
-        constexpr uint32_t kTd = kTile >> 4, kSd = kSlab >> 4, kEd = kExt >> 4;
-        const bool lead = lane == 0;
-        auto wait_m = [&](int b, int k) {
-            wait_k(b, k);
-            tc_fence_after();
-        };
-        for (int i = 0; i < count && wt.ok; ++i) {
-            const int t0 = chunk_of(i) * kT, n = min(kT, len - t0), eb = i & 1;
-            const uint64_t desi = des + eb * kTd;
-            // rows of the tensor behind this sequence may hold anything: cleared in the slice,
-            // since they enter sums over tokens (rows past L arrive as zero)
-            const bool clear = n < kT && t0 + n < p.L;
-            auto slice = [&](int s) {   // F-side slice s of the chunk, complete and clean
-                const int u = i * nsE + s, sl = u & 3;
-                wait_m(B_FSF + sl, u >> 2);
-                if (clear) {
-                    for (int a = n * 8 + lane; a < kT * 8; a += 32)
-                        st_shared_v4(sbase + Lo.fs + sl * kTile + a * 16, 0u, 0u, 0u, 0u);
+        } else if (warp == 0) {
+            // -------------------------------------------------------------- MMA issue
+            constexpr uint32_t idP = idesc_bf16(128, 128, 0, 0);
+            constexpr uint32_t idKM = idesc_bf16(128, 64, 0, 1);    // A K-major (or tensor memory), B MN-major
+            constexpr uint32_t idKK = idesc_bf16(128, 64, 0, 0);
+            constexpr uint32_t idMM = idesc_bf16(128, 64, 1, 1);
+            constexpr uint32_t idMM2 = idesc_bf16(128, 128, 1, 1);
+            constexpr uint32_t idMz = idesc_bf16(128, 16, 1, 0);
+            constexpr uint32_t idKz = idesc_bf16(128, 16, 0, 0);
+            constexpr uint32_t kTd = kTile >> 4, kSd = kSlab >> 4, kEd = kExt >> 4;
+            const uint64_t d0 = sdesc(sbase, 16, 1024, kLayoutSW128);
+            const uint64_t dT = sdesc(sbase, kTile, 1024, kLayoutSW128);   // the next 64 rows or columns one tile on
+            constexpr uint32_t oFs = Lo.fs >> 4, oFq = Lo.fq >> 4, oEs = Lo.es >> 4, oEq = Lo.eq >> 4, oY = Lo.y >> 4,
+                               oM = Lo.m >> 4, oZe = Lo.zext >> 4, oWe = Lo.wext >> 4;
+            auto wait_m = [&](int b, int k) {
+                wait_k(b, k);
+                tc_fence_after();
+            };
+            for (int i = 0; i < count && wt.ok; ++i) {
+                const int t0 = chunk_of(i) * kT, n = min(kT, len - t0), eb = i & 1;
+                // rows of the tensor behind this sequence may hold anything: cleared in the
+                // tiles, since they enter sums over tokens (rows past L arrive as zero)
+                const bool clear = n < kT && t0 + n < p.L;
+                auto clear_rows = [&](uint32_t tile) {
+                    for (int a = n * 8 + lane; a < kT * 8; a += 32) st_shared_v4(sbase + tile + a * 16, 0u, 0u, 0u, 0u);
                     fence_async_smem();
                     __syncwarp();
-                }
-                return sl;
-            };
-            auto state_pair = [&](int s) {   // T of the pair whose last slice is s
-                const uint64_t da = dfsT + ((i * nsE + (s & ~1)) & 3) * kTd;
-                const uint32_t t = tmem + kColT + kTStride * (s >> 1);
-                for (int l = 0; l < nl; ++l)
+                };
+                auto slice = [&](int s) {   // F-side slice s of the chunk, complete and clean
+                    const int u = i * nsE + s, sl = u & 3;
+                    wait_m(B_FSF + sl, u >> 2);
+                    if (clear) clear_rows(Lo.fs + sl * kTile);
+                    return sl;
+                };
+                auto state_pair = [&](int s) {   // T of the pair of slices s, s + 1
+                    const uint64_t da = dT + oFs + ((i * nsE + s) & 3) * kTd;
+                    const uint32_t t = tmem + col_t(kMode) + t_stride(kMode) * (s >> 1);
+                    const uint32_t oy = oY + (kMode == kState ? eb * 3 * kTd : 0);
+                    int l = 0;
+                    if (kMode != kOutE && nl > 1) {   // two limbs side by side: the F side is read once
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_bf16(t, da + 128 * kk, dy + l * kTd + 128 * kk, idMM, (l > 0 || kk > 0) ? 1u : 0u);
-                if (p.has_z)
+                        for (int kk = 0; kk < 8; ++kk) umma_bf16(t, da + 128 * kk, dT + oy + 128 * kk, idMM2, kk > 0 ? 1u : 0u);
+                        l = 2;
+                    }
+                    for (; l < nl; ++l)
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_bf16(t + 64, da + 128 * kk, dwe + (kk >> 2) * kEd + 2 * (kk & 3), idMz, kk > 0 ? 1u : 0u);
-            };
-            auto free_pair = [&](int s) {
-                const int sl = (i * nsE + (s & ~1)) & 3;
-                umma_commit(&bar[B_FSE + sl]);
-                umma_commit(&bar[B_FSE + sl + 1]);
-            };
-            if (kMode == kOutE) {
-                wait_m(B_ESF + eb, i >> 1);
-                const int v = i * ns - 1, vo = (v & 1) ? v : v - 1;   // last use of the buffer over P
-                if (vo >= 1) wait_m(B_OE + 1, vo >> 1);
-                if (lead) {
-                    const uint64_t deqi = deq + eb * kTd;
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_bf16(t, da + 128 * kk, d0 + oy + l * kTd + 128 * kk, idMM, (l > 0 || kk > 0) ? 1u : 0u);
+                    if (has_z) {
+                        const uint64_t dw = d0 + oWe + (kMode == kState ? eb * 2 * kEd : 0);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16(tmem + kColP, deqi + 2 * kk, desi + 2 * kk, idP, kk > 0 ? 1u : 0u);
-                    umma_commit(&bar[B_PF]);
-                }
-            }
-            for (int s = 0; s < ns; ++s) {
-                const int sl = slice(s);
-                const bool pair_done = (s & 1) || s == ns - 1;
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_bf16(t + col_z(kMode), da + 128 * kk, dw + (kk >> 2) * kEd + 2 * (kk & 3), idMz, kk > 0 ? 1u : 0u);
+                    }
+                };
+                auto free_pair = [&](int s) {
+                    const int sl = (i * nsE + s) & 3;
+                    umma_commit(&bar[B_FSE + sl]);
+                    umma_commit(&bar[B_FSE + sl + 1]);
+                };
+                const uint64_t des = d0 + oEs + eb * kTd, deq = d0 + oEq + eb * kTd;
                 if (kMode == kOutF) {
-                    const int u2 = i * ns + s, q = u2 & 1;
-                    wait_m(B_FQF + q, u2 >> 1);
-                    const uint64_t dx = dfq + q * kTd, dyy = dfs + sl * kTd;
-                    if (lead) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_bf16(tmem + kColP, dx + 2 * kk, dyy + 2 * kk, idP, (s > 0 || kk > 0) ? 1u : 0u);
-                        if (s == ns - 1) umma_commit(&bar[B_PF]);
-                    }
-                    if (s == 0) {
-                        wait_m(B_MF, i);
-                        if (i >= 1) wait_m(B_OE, i - 1);
-                    }
-                    if (lead) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_bf16(tmem + kColO + 64, dx + 2 * kk, dm + s * kSd + 128 * kk, idKM,
-                                      (s > 0 || kk > 0) ? 1u : 0u);
-                        if (p.has_den)
+                    // the scores and the state's part take the place of the last chunk's outputs
+                    if (i >= 1) wait_m(B_OE, i - 1);
+                    for (int s = 0; s < ns; ++s) {
+                        const int sl = slice(s), u2 = i * ns + s, q = u2 & 1;
+                        wait_m(B_FQF + q, u2 >> 1);
+                        const uint64_t dx = d0 + oFq + q * kTd, dyy = d0 + oFs + sl * kTd;
+                        if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16(tmem + kColO + 128, dx + 2 * kk, dze + s * kEd + 2 * kk, idKz,
+                                umma_bf16(tmem + kColP, dx + 2 * kk, dyy + 2 * kk, idP, (s > 0 || kk > 0) ? 1u : 0u);
+                            if (s == ns - 1) umma_commit(&bar[B_PF]);
+                        }
+                        if (s == 0) wait_m(B_MF, i);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_bf16(tmem + kColOe, dx + 2 * kk, d0 + oM + s * kSd + 128 * kk, idKM,
                                           (s > 0 || kk > 0) ? 1u : 0u);
-                        umma_commit(&bar[B_FQE + q]);
-                    }
-                }
-                if (!pair_done) continue;
-                if (s <= 1) {
-                    wait_m(B_YF, i);
-                    if (kMode != kOutF) wait_m(B_MF, i);
-                }
-                if (lead) state_pair(s);
-                if (kMode == kOutE) {
-                    if (s <= 1) wait_m(B_PT, i);
-                    for (int r = s & ~1; r <= s; ++r) {
-                        const int v = i * ns + r, ob = v & 1;
-                        if (v >= 2) wait_m(B_OE + ob, (v >> 1) - 1);
-                        const uint32_t oi = tmem + (ob ? kColP : kColO);
-                        const uint64_t du = dfs + ((i * nsE + r) & 3) * kTd, deqi = deq + eb * kTd;
-                        if (lead) {
+                            if (kDen)
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
-                                umma_bf16_ts(oi, tmem + kColPt + 8 * kk, du + 128 * kk, idKM, kk > 0 ? 1u : 0u);
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16(oi + 64, deqi + 2 * kk, dm + r * kSd + 2 * kk, idKK, kk > 0 ? 1u : 0u);
-                            umma_commit(&bar[B_OF + ob]);
+                                for (int kk = 0; kk < 4; ++kk)
+                                    umma_bf16(tmem + kColDen, dx + 2 * kk, d0 + oZe + s * kEd + 2 * kk, idKz,
+                                              (s > 0 || kk > 0) ? 1u : 0u);
+                            umma_commit(&bar[B_FQE + q]);
                         }
                     }
-                }
-                if (lead) free_pair(s);
-            }
-            if (lead) umma_commit(&bar[B_TF]);
-            if (kMode == kOutF) {
-                wait_m(B_PT, i);
-                if (lead) {
+                    wait_m(B_YF, i);
+                    if (elect_one()) {
+                        for (int s = 0; s < ns; s += 2) {
+                            state_pair(s);
+                            free_pair(s);
+                        }
+                        umma_commit(&bar[B_TF]);
+                    }
+                    wait_m(B_PT, i);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_bf16_ts(tmem + kColO, tmem + kColPt + 8 * kk, desi + 128 * kk, idKM, kk > 0 ? 1u : 0u);
-                    umma_commit(&bar[B_OF]);
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_bf16_ts(tmem + kColOi, tmem + kColP + 8 * kk, des + 128 * kk, idKM, kk > 0 ? 1u : 0u);
+                        umma_commit(&bar[B_OF]);
+                        umma_commit(&bar[B_ESE + eb]);
+                    }
+                } else if (kMode == kOutE) {
+                    wait_m(B_ESF + eb, i >> 1);
+                    if (clear) clear_rows(Lo.es + eb * kTile);
+                    const int v1 = i * ns - 1, vo = (v1 & 1) ? v1 : v1 - 1;   // last use of the buffer over P
+                    if (vo >= 1) wait_m(B_OE + 1, vo >> 1);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_bf16(tmem + kColP, deq + 2 * kk, des + 2 * kk, idP, kk > 0 ? 1u : 0u);
+                        umma_commit(&bar[B_PF]);
+                    }
+                    wait_m(B_YF, i);
+                    for (int s = 0; s < ns; s += 2) {
+                        slice(s);
+                        if (s + 1 < ns) slice(s + 1);
+                        if (elect_one()) {
+                            state_pair(s);
+                            if (s + 2 >= ns) umma_commit(&bar[B_TF]);
+                        }
+                        if (s == 0) {
+                            wait_m(B_PT, i);
+                            wait_m(B_MF, i);
+                        }
+                        for (int r = s; r < min(s + 2, ns); ++r) {
+                            const int v = i * ns + r, ob = v & 1;
+                            if (v >= 2) wait_m(B_OE + ob, (v >> 1) - 1);
+                            const uint32_t oi = tmem + (ob ? kColOi : kColOi0), oe = tmem + (ob ? kColOe1 : kColOe0);
+                            const uint64_t du = d0 + oFs + ((i * nsE + r) & 3) * kTd;
+                            if (elect_one()) {
+#pragma unroll
+                                for (int kk = 0; kk < 8; ++kk)
+                                    umma_bf16_ts(oi, tmem + kColP + 8 * kk, du + 128 * kk, idKM, kk > 0 ? 1u : 0u);
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    umma_bf16(oe, deq + 2 * kk, d0 + oM + r * kSd + 2 * kk, idKK, kk > 0 ? 1u : 0u);
+                                umma_commit(&bar[B_OF + ob]);
+                            }
+                        }
+                        if (elect_one()) free_pair(s);
+                    }
+                    if (elect_one()) {
+                        umma_commit(&bar[B_OD]);
+                        umma_commit(&bar[B_ESE + eb]);
+                    }
+                } else {
+                    wait_m(B_YF + eb, i >> 1);
+                    wait_m(B_MF, i);
+                    for (int s = 0; s < ns; s += 2) {
+                        slice(s);
+                        if (s + 1 < ns) slice(s + 1);
+                        if (elect_one()) {
+                            state_pair(s);
+                            free_pair(s);
+                        }
+                    }
+                    if (elect_one()) {
+                        umma_commit(&bar[B_TF]);
+                        umma_commit(&bar[B_ESE + eb]);
+                    }
                 }
+                __syncwarp();
             }
-            if (lead) umma_commit(&bar[B_ESE + eb]);
-            __syncwarp();
         }
         __syncwarp();
     } else {
         // ------------------------------------------------------------------ epilogue
-        // (no early exit on a wait that ran out: the named barriers want every warp)
-        const int q = warp & 3, half = (warp - 2) >> 2;
-        const int row = 32 * q + lane;           // token of scores and outputs; feature of T
+        // (no early exit on a wait that ran out: the pairs of warps share named barriers)
+        regs_inc<208>();
+        const int q = warp & 3, ew = warp - 4, half = ew >> 2;
+        const int row = 32 * q + lane;   // token of scores, outputs and weighted rows; feature of T
         const uint32_t trow = tmem + ((32u * q) << 16);
         const float* pw = reinterpret_cast<const float*>(sm + Lo.pw);
         float* smul = reinterpret_cast<float*>(sm + Lo.smul);
@@ -356,7 +434,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
         float* dsum = reinterpret_cast<float*>(sm + Lo.dsum);
         float* zf = reinterpret_cast<float*>(sm + Lo.zf);
         const int64_t sidx = static_cast<int64_t>(bh) * p.nseg + seg;
-        float run[2][32], zrun = 0.0f;           // M at (f = 128 b + row, e = 32 half + c); z at b = half
+        float run[2][32], zrun = 0.0f;   // M at (f = 128 b + row, e = 32 half + c); z at b = half
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const int f = 128 * b + row;
@@ -370,7 +448,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 run[b][4 * c + 2] = w.z;
                 run[b][4 * c + 3] = w.w;
             }
-            if (b == half && in && p.has_z) zrun = p.first_z[sidx * p.F + f0 + f];
+            if (b == half && in && has_z) zrun = p.first_z[sidx * p.F + f0 + f];
         }
         // the operand copy of M, and its z column, for chunk i
         auto write_m = [&](int i) {
@@ -384,7 +462,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                         st_shared_v4(slab + sw128_off(f & 63, 4 * half + c),
                                      pack_bf16(run[b][8 * c], run[b][8 * c + 1]), pack_bf16(run[b][8 * c + 2], run[b][8 * c + 3]),
                                      pack_bf16(run[b][8 * c + 4], run[b][8 * c + 5]), pack_bf16(run[b][8 * c + 6], run[b][8 * c + 7]));
-                    if (b == half && p.has_z) {
+                    if (b == half && has_z) {
                         if (kMode == kOutF) {
                             uint16_t l[3];
                             limbs3(zrun, l);
@@ -398,6 +476,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 }
             }
             fence_async_smem();
+            warp_arrive(&bar[B_MF]);
         };
         // the weighted rows of chunk i (this thread: token `row`, 32 of its columns) in limbs,
         // the z weights and the score scalars of its tokens
@@ -405,184 +484,299 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
             const int t0 = chunk_of(i) * kT, n = min(kT, len - t0), eb = i & 1;
             const bool in = row < n;
             const int64_t grow = static_cast<int64_t>(bh) * p.L + t0 + row;
-            const float mul = in && p.s_mul ? p.s_mul[grow] : 1.0f;
-            const float off = in && p.s_off ? p.s_off[grow] : 0.0f;
-            const float w = in ? decay_pow(g2, p.rev ? row + 1 : n - 1 - row) : 0.0f;
+            const float mul = kCols && in ? p.s_mul[grow] : 1.0f;
+            const float off = kCols && in ? p.s_off[grow] : 0.0f;
+            const float w = in ? decay_pow(g2, kRev ? row + 1 : n - 1 - row) : 0.0f;
             const float a = w * mul;
+            const uint32_t ybase = sbase + Lo.y + (kMode == kState ? eb * 3 * kTile : 0);
             wait_k(B_ESF + eb, i >> 1);
+            uint4 r[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                r[c] = *reinterpret_cast<const uint4*>(sm + Lo.es + eb * kTile + sw128_off(row, 4 * half + c));
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const uint32_t o = sw128_off(row, 4 * half + c);
-                uint4* src = reinterpret_cast<uint4*>(sm + Lo.es + eb * kTile + o);
-                const uint4 r = *src;
-                uint32_t v[4] = {r.x, r.y, r.z, r.w};
+                uint32_t v[4] = {r[c].x, r[c].y, r[c].z, r[c].w};
                 if (!in) {
                     v[0] = v[1] = v[2] = v[3] = 0u;
-                    if (kMode == kOutF) *src = make_uint4(0u, 0u, 0u, 0u);   // they are an operand as they are, too
+                    if (kMode == kOutF) st_shared_v4(sbase + Lo.es + eb * kTile + o, 0u, 0u, 0u, 0u);   // an operand itself
                 }
                 if (nl == 1) {
-                    st_shared_v4(sbase + Lo.y + o, v[0], v[1], v[2], v[3]);
+                    st_shared_v4(ybase + o, v[0], v[1], v[2], v[3]);
                     continue;
                 }
-                uint32_t l[3][4];
+                float2 y[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float y0 = a * bf_lo(v[e]), y1 = a * bf_hi(v[e]);
+                for (int e = 0; e < 4; ++e) y[e] = fmul2(make_float2(a, a), make_float2(bf_lo(v[e]), bf_hi(v[e])));
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        l[k][e] = pack_bf16(y0, y1);
-                        y0 -= bf_lo(l[k][e]);
-                        y1 -= bf_hi(l[k][e]);
+                for (int k = 0; k < 3; ++k) {
+                    if (k >= nl) break;
+                    uint32_t l[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        l[e] = pack_bf16(y[e].x, y[e].y);
+                        y[e] = ffma2(make_float2(-1.0f, -1.0f), make_float2(bf_lo(l[e]), bf_hi(l[e])), y[e]);
                     }
+                    st_shared_v4(ybase + k * kTile + o, l[0], l[1], l[2], l[3]);
                 }
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    st_shared_v4(sbase + Lo.y + k * kTile + o, l[k][0], l[k][1], l[k][2], l[k][3]);
             }
             if (half == 0) {
-                if (p.has_z) {
+                if (has_z) {
                     uint16_t l[3];
-                    limbs3(p.z_delta ? -a * off : w, l);
-                    const uint32_t t = sbase + Lo.wext + (row >> 6) * kExt;
+                    limbs3(kCols ? -a * off : w, l);
+                    const uint32_t t = sbase + Lo.wext + (kMode == kState ? eb * 2 * kExt : 0) + (row >> 6) * kExt;
 #pragma unroll
                     for (int k = 0; k < 3; ++k) st_shared_u16(t + sw128_off(k, (row & 63) >> 3) + (row & 7) * 2, l[k]);
                 }
-                smul[(i & 1) * kT + row] = mul;
-                soff[(i & 1) * kT + row] = off;
+                if (kCols) {
+                    smul[(i & 1) * kT + row] = mul;
+                    soff[(i & 1) * kT + row] = off;
+                }
             }
             fence_async_smem();
-            warp_arrive(&bar[B_YF]);
+            warp_arrive(&bar[kMode == kState ? B_YF + eb : B_YF]);
+        };
+        // M <- lambda^n M + T
+        auto update_m = [&](int i) {
+            const int n = min(kT, len - chunk_of(i) * kT);
+            const float lam = decay_pow(g2, n);
+            const bool two = kMode != kOutE && nl > 1;
+            wait_k(B_TF, i);
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if (2 * b >= ns) break;
+                const uint32_t tc = trow + col_t(kMode) + t_stride(kMode) * b;
+                uint32_t t[32], t2[32], z0 = 0, z1 = 0, z2 = 0;
+                tmem_ld32(tc + 32 * half, t);
+                if (two) tmem_ld32(tc + 64 + 32 * half, t2);
+                if (has_z && b == half) {
+                    tmem_ld1(tc + col_z(kMode), z0);
+                    tmem_ld1(tc + col_z(kMode) + 1, z1);
+                    tmem_ld1(tc + col_z(kMode) + 2, z2);
+                }
+                tmem_wait_ld();
+                reg_fence(t);
+                reg_fence(t2);
+                reg_fence1(z0);
+                reg_fence1(z1);
+                reg_fence1(z2);
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    float2 w = make_float2(__uint_as_float(t[c]), __uint_as_float(t[c + 1]));
+                    if (two) w = fadd2(w, make_float2(__uint_as_float(t2[c]), __uint_as_float(t2[c + 1])));
+                    const float2 r = ffma2(make_float2(lam, lam), make_float2(run[b][c], run[b][c + 1]), w);
+                    run[b][c] = r.x;
+                    run[b][c + 1] = r.y;
+                }
+                if (has_z && b == half)
+                    zrun = fmaf(lam, zrun, __uint_as_float(z0) + (__uint_as_float(z1) + __uint_as_float(z2)));
+            }
+            tc_fence_before();
+        };
+        // the scalars of four query / state tokens: off the raw scores, onto the weights
+        auto scale = [&](int par, int j, float2 off, float2& s0, float2& s1, float2& w0, float2& w1) {
+            if (kRows) {
+                s0 = fadd2(s0, off);
+                s1 = fadd2(s1, off);
+            }
+            if (kCols) {
+                const float4 m = *reinterpret_cast<const float4*>(smul + par * kT + j);
+                w0 = fmul2(w0, make_float2(m.x, m.y));
+                w1 = fmul2(w1, make_float2(m.z, m.w));
+                if (kMode == kOutE) {
+                    const float4 o = *reinterpret_cast<const float4*>(soff + par * kT + j);
+                    s0 = fadd2(s0, make_float2(-o.x, -o.y));
+                    s1 = fadd2(s1, make_float2(-o.z, -o.w));
+                }
+            }
+        };
+        // Masked, decayed scores -> P~.  A warp has two 32-column blocks of its 32 rows; a block
+        // is wholly inside the mask (lambda^(i-j) as a row times a column factor, both <= 1), on
+        // the diagonal, or wholly outside.  Returns the sum over this thread's columns.
+        auto scores = [&](int i, float qo, float qm) {
+            const int par = i & 1;
+            if (kCols) wait_k(B_YF, i);   // smul, soff of this chunk
+            wait_k(B_PF, i);
+            tc_fence_after();
+            float2 rs = make_float2(0.0f, 0.0f);
+            uint32_t pk[2][16];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const int cb = half + 2 * hh, j0 = 32 * cb;
+                const int side = kRev ? cb - q : q - cb;   // > 0: inside, 0: diagonal
+                if (side < 0) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) pk[hh][c] = 0u;
+                    continue;
+                }
+                uint32_t r[32];
+                tmem_ld32(trow + kColP + j0, r);
+                tmem_wait_ld();
+                reg_fence(r);
+                // (query rows behind the sequence keep whatever comes out: it reaches their own
+                // output rows only, which are not stored)
+                const float2 off = make_float2(-qo, -qo);
+                if (side > 0) {
+                    const float f = qm * decay_pow(g2, kRev ? j0 - row : row - j0 - 31);
+                    const float2 rf = make_float2(f, f);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(pw + 64 + c);
+                        float2 w0 = fmul2(rf, make_float2(t.x, t.y)), w1 = fmul2(rf, make_float2(t.z, t.w));
+                        float2 s0 = make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+                        float2 s1 = make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
+                        scale(par, j0 + c, off, s0, s1, w0, w1);
+                        if (kDen) {
+                            rs = ffma2(s0, w0, rs);
+                            rs = ffma2(s1, w1, rs);
+                        }
+                        s0 = fmul2(s0, w0);
+                        s1 = fmul2(s1, w1);
+                        pk[hh][c / 2] = pack_bf16(s0.x, s0.y);
+                        pk[hh][c / 2 + 1] = pack_bf16(s1.x, s1.y);
+                    }
+                } else {
+                    const float* pd = pw + 31 + (kRev ? -lane : lane);
+                    const float2 rf = make_float2(qm, qm);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        float2 w0 = make_float2(pd[kRev ? c : -c], pd[kRev ? c + 1 : -c - 1]);
+                        float2 w1 = make_float2(pd[kRev ? c + 2 : -c - 2], pd[kRev ? c + 3 : -c - 3]);
+                        if (kRows) {
+                            w0 = fmul2(rf, w0);
+                            w1 = fmul2(rf, w1);
+                        }
+                        float2 s0 = make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+                        float2 s1 = make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
+                        scale(par, j0 + c, off, s0, s1, w0, w1);
+                        s0 = fmul2(s0, w0);
+                        s1 = fmul2(s1, w1);
+                        // (what is masked may be infinite: selected, not multiplied away)
+                        if (kRev ? c < lane : c > lane) s0.x = 0.0f;
+                        if (kRev ? c + 1 < lane : c + 1 > lane) s0.y = 0.0f;
+                        if (kRev ? c + 2 < lane : c + 2 > lane) s1.x = 0.0f;
+                        if (kRev ? c + 3 < lane : c + 3 > lane) s1.y = 0.0f;
+                        if (kDen) {
+                            rs.x += s0.x + s1.x;
+                            rs.y += s0.y + s1.y;
+                        }
+                        pk[hh][c / 2] = pack_bf16(s0.x, s0.y);
+                        pk[hh][c / 2 + 1] = pack_bf16(s1.x, s1.y);
+                    }
+                }
+            }
+            if (kMode == kOutF && kDen) dsum[(par * 2 + half) * kT + row] = rs.x + rs.y;
+            // P~ goes over the scores once both warps of these rows have read theirs
+            tc_fence_before();
+            named_bar_sync(1 + q, 64);
+            tc_fence_after();
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) tmem_st16(trow + kColP + 16 * (half + 2 * hh), pk[hh]);
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&bar[B_PT]);
         };
         if (count > 0) {
-            if (kMode != kState) write_m(0);
-            warp_arrive(&bar[B_MF]);
+            if (kMode != kState) write_m(0); else warp_arrive(&bar[B_MF]);
             write_y(0);
-            named_bar_sync(1, 256);
         }
         for (int i = 0; i < count; ++i) {
+            const bool more = i + 1 < count;
+            if (kMode == kState) {
+                if (more) write_y(i + 1);   // the other limb buffer: off the state's chain
+                update_m(i);
+                if (more) warp_arrive(&bar[B_MF]);   // T has been read
+                continue;
+            }
             const int t0 = chunk_of(i) * kT, n = min(kT, len - t0), par = i & 1;
             const int64_t grow = static_cast<int64_t>(bh) * p.L + t0 + row;
             const bool valid = row < n;
-            float fac = decay_pow(g2, p.rev ? max(n - 1 - row, 0) : row + 1), qo = 0.0f, qm = 1.0f;
-            if (kMode == kOutE && valid) {
-                if (p.q_mul) qm = p.q_mul[grow];
-                if (p.q_off) qo = p.q_off[grow];
-            }
-            if (kMode != kState) {
-                // masked, decayed scores -> P~ (this warp's half of the columns)
-                wait_k(B_PF, i);
-                tc_fence_after();
-                float rs = 0.0f;
-                const bool cols = p.s_mul != nullptr;
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    uint32_t r[32], pk[16];
-                    tmem_ld32(trow + kColP + 64 * half + 32 * hh, r);
-                    tmem_wait_ld();
-                    reg_fence(r);
-                    const int j0 = 64 * half + 32 * hh;
-                    float w[32];
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const int j = j0 + c, d = p.rev ? j - row : row - j;
-                        float sc = __uint_as_float(r[c]);
-                        if (kMode == kOutE) sc -= qo;
-                        if (cols) sc = (kMode == kOutE ? sc - soff[par * kT + j] : sc) * smul[par * kT + j];
-                        w[c] = d >= 0 && j < n ? sc * pw[max(d, 0)] : 0.0f;
-                    }
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        if (kMode == kOutE) { w[2 * c] *= qm; w[2 * c + 1] *= qm; }
-                        if (kMode == kOutF) rs += w[2 * c] + w[2 * c + 1];
-                        pk[c] = pack_bf16(w[2 * c], w[2 * c + 1]);
-                    }
-                    tmem_st16(trow + kColPt + 32 * half + 16 * hh, pk);
-                }
-                tmem_wait_st();
-                if (kMode == kOutF && p.has_den) dsum[(par * 2 + half) * kT + row] = rs;
-                tc_fence_before();
-                warp_arrive(&bar[B_PT]);
-            }
+            const float fac = decay_pow(g2, kRev ? max(n - 1 - row, 0) : row + 1);
             if (kMode == kOutE) {
-                // outputs, 64 features at a time
-                const float fq = fac * qm, zc = p.q_off ? -qo : 1.0f;
+                float qo = 0.0f, qm = 1.0f;
+                if (kRows && valid) {
+                    qm = p.q_mul[grow];
+                    qo = p.q_off[grow];
+                }
+                scores(i, qo, qm);
+                // outputs, 64 features at a time; through the warp's staging box and a TMA store
+                // unless rows of the tensor behind the sequence have to stay
+                const float fq = fac * qm, zc = kRows ? -qo : 1.0f;
+                const bool whole = n == kT || t0 + n == p.L;
+                const uint32_t box = sbase + Lo.stg + ew * 2048;
+                if (has_z) wait_k(B_MF, i);   // zf of this chunk
                 for (int s = 0; s < ns; ++s) {
                     const int v = i * ns + s, ob = v & 1;
                     wait_k(B_OF + ob, v >> 1);
                     tc_fence_after();
                     uint32_t a[32], e[32];
-                    const uint32_t oc = trow + (ob ? kColP : kColO) + 32 * half;
-                    tmem_ld32(oc, a);
-                    tmem_ld32(oc + 64, e);
+                    tmem_ld32(trow + (ob ? kColOi : kColOi0) + 32 * half, a);
+                    tmem_ld32(trow + (ob ? kColOe1 : kColOe0) + 32 * half, e);
                     tmem_wait_ld();
                     reg_fence(a);
                     reg_fence(e);
                     tc_fence_before();
                     warp_arrive(&bar[B_OE + ob]);
                     const int fl = 64 * s + 32 * half;
-                    __nv_bfloat16* dst = p.o + grow * p.F + f0 + fl;
-                    const float4* z4 = reinterpret_cast<const float4*>(zf + par * kMaxFw + fl);
+                    if (has_z) {
+                        const float4* z4 = reinterpret_cast<const float4*>(zf + par * kMaxFw + fl);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float t[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) t[k] = __uint_as_float(e[8 * c + k]);
-                        if (p.has_z) {
-                            const float4 z0 = z4[2 * c], z1 = z4[2 * c + 1];
-                            t[0] = fmaf(zc, z0.x, t[0]); t[1] = fmaf(zc, z0.y, t[1]);
-                            t[2] = fmaf(zc, z0.z, t[2]); t[3] = fmaf(zc, z0.w, t[3]);
-                            t[4] = fmaf(zc, z1.x, t[4]); t[5] = fmaf(zc, z1.y, t[5]);
-                            t[6] = fmaf(zc, z1.z, t[6]); t[7] = fmaf(zc, z1.w, t[7]);
+                        for (int c = 0; c < 8; ++c) {
+                            const float4 z = z4[c];
+                            e[4 * c] = __float_as_uint(fmaf(zc, z.x, __uint_as_float(e[4 * c])));
+                            e[4 * c + 1] = __float_as_uint(fmaf(zc, z.y, __uint_as_float(e[4 * c + 1])));
+                            e[4 * c + 2] = __float_as_uint(fmaf(zc, z.z, __uint_as_float(e[4 * c + 2])));
+                            e[4 * c + 3] = __float_as_uint(fmaf(zc, z.w, __uint_as_float(e[4 * c + 3])));
                         }
+                    }
+                    uint32_t o[16];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) t[k] = fmaf(fq, t[k], __uint_as_float(a[8 * c + k]));
-                        if (valid && fl + 8 * c < fv)
-                            *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(pack_bf16(t[0], t[1]), pack_bf16(t[2], t[3]),
-                                                                                pack_bf16(t[4], t[5]), pack_bf16(t[6], t[7]));
+                    for (int c = 0; c < 16; ++c)
+                        o[c] = pack_bf16(fmaf(fq, __uint_as_float(e[2 * c]), __uint_as_float(a[2 * c])),
+                                         fmaf(fq, __uint_as_float(e[2 * c + 1]), __uint_as_float(a[2 * c + 1])));
+                    if (whole) {
+                        if (lane == 0) bulk_wait_read<0>();   // the box's last store has read it
+                        __syncwarp();
+                        const uint32_t rsw = (static_cast<uint32_t>(lane) >> 1) & 3u;   // 64-byte swizzle
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            st_shared_v4(box + lane * 64u + ((static_cast<uint32_t>(c) ^ rsw) << 4), o[4 * c], o[4 * c + 1],
+                                         o[4 * c + 2], o[4 * c + 3]);
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && fl < fv) {
+                            tma_store_3d(&tout, sm + Lo.stg + ew * 2048, f0 + fl, t0 + 32 * q, bh);
+                            bulk_commit_group();
+                        }
+                    } else if (valid) {
+                        __nv_bfloat16* dst = p.o + grow * p.F + f0 + fl;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (fl + 8 * c < fv)
+                                *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                     }
                 }
-            }
-            // the state that leaves the chunk
-            wait_k(B_TF, i);
-            tc_fence_after();
-            const float lam = decay_pow(g2, n);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (2 * b >= ns) break;
-                uint32_t t[32], z0 = 0, z1 = 0, z2 = 0;
-                tmem_ld32(trow + kColT + kTStride * b + 32 * half, t);
-                if (p.has_z && b == half) {
-                    tmem_ld1(trow + kColT + kTStride * b + 64, z0);
-                    tmem_ld1(trow + kColT + kTStride * b + 65, z1);
-                    tmem_ld1(trow + kColT + kTStride * b + 66, z2);
+                update_m(i);
+                if (more) {
+                    wait_k(B_OD, i);   // the state's operand is read until the chunk's last output
+                    write_m(i + 1);
+                    write_y(i + 1);
                 }
-                tmem_wait_ld();
-                reg_fence(t);
-                reg_fence1(z0);
-                reg_fence1(z1);
-                reg_fence1(z2);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) run[b][c] = fmaf(lam, run[b][c], __uint_as_float(t[c]));
-                if (p.has_z && b == half)
-                    zrun = fmaf(lam, zrun, __uint_as_float(z0) + (__uint_as_float(z1) + __uint_as_float(z2)));
-            }
-            tc_fence_before();
-            if (i + 1 < count) {
-                if (kMode != kState) write_m(i + 1);
-                warp_arrive(&bar[B_MF]);
-                write_y(i + 1);
-            }
-            if (kMode != kState) named_bar_sync(1, 256);
-            if (kMode == kOutF) {
+            } else {
+                scores(i, 0.0f, 1.0f);
+                update_m(i);
+                if (more) write_m(i + 1);   // the next chunk's products want the state first
                 wait_k(B_OF, i);
                 tc_fence_after();
                 uint32_t a[32], e[32], d0 = 0, d1 = 0, d2 = 0;
-                tmem_ld32(trow + kColO + 32 * half, a);
-                tmem_ld32(trow + kColO + 64 + 32 * half, e);
-                if (p.has_den) {
-                    tmem_ld1(trow + kColO + 128, d0);
-                    tmem_ld1(trow + kColO + 129, d1);
-                    tmem_ld1(trow + kColO + 130, d2);
+                tmem_ld32(trow + kColOi + 32 * half, a);
+                tmem_ld32(trow + kColOe + 32 * half, e);
+                if (kDen) {
+                    tmem_ld1(trow + kColDen, d0);
+                    tmem_ld1(trow + kColDen + 1, d1);
+                    tmem_ld1(trow + kColDen + 2, d2);
                 }
                 tmem_wait_ld();
                 reg_fence(a);
@@ -592,47 +786,65 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 reg_fence1(d2);
                 tc_fence_before();
                 warp_arrive(&bar[B_OE]);
-                if (valid) {
-                    float t[32], dn = 0.0f;
+                float t[32], dn = 0.0f;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) t[c] = fmaf(fac, __uint_as_float(e[c]), __uint_as_float(a[c]));
-                    if (p.has_den)
-                        dn = fmaf(fac, __uint_as_float(d0) + (__uint_as_float(d1) + __uint_as_float(d2)),
-                                  dsum[par * 2 * kT + row] + dsum[(par * 2 + 1) * kT + row]);
-                    if (p.part_mode) {
-                        float4* pp = reinterpret_cast<float4*>(p.part + grow * 64 + 32 * half);
-                        if (p.part_mode == 1) {
+                for (int c = 0; c < 32; ++c) t[c] = fmaf(fac, __uint_as_float(e[c]), __uint_as_float(a[c]));
+                if (kDen)
+                    dn = fmaf(fac, __uint_as_float(d0) + (__uint_as_float(d1) + __uint_as_float(d2)),
+                              dsum[par * 2 * kT + row] + dsum[(par * 2 + 1) * kT + row]);
+                if (p.part_mode && valid) {
+                    float4* pp = reinterpret_cast<float4*>(p.part + grow * 64 + 32 * half);
+                    if (p.part_mode == 1) {
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) pp[c] = make_float4(t[4 * c], t[4 * c + 1], t[4 * c + 2], t[4 * c + 3]);
-                            if (half == 0) p.part_den[grow] = dn;
-                        } else {
+                        for (int c = 0; c < 8; ++c) pp[c] = make_float4(t[4 * c], t[4 * c + 1], t[4 * c + 2], t[4 * c + 3]);
+                        if (half == 0) p.part_den[grow] = dn;
+                    } else {
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const float4 w = pp[c];
-                                t[4 * c] += w.x;
-                                t[4 * c + 1] += w.y;
-                                t[4 * c + 2] += w.z;
-                                t[4 * c + 3] += w.w;
-                            }
-                            dn += p.part_den[grow];
+                        for (int c = 0; c < 8; ++c) {
+                            const float4 w = pp[c];
+                            t[4 * c] += w.x;
+                            t[4 * c + 1] += w.y;
+                            t[4 * c + 2] += w.z;
+                            t[4 * c + 3] += w.w;
                         }
-                    }
-                    if (p.part_mode != 1) {
-                        if (p.has_den) {
-                            if (p.den && half == 0) p.den[grow] = dn;
-                            const float rd = 1.0f / (dn + p.eps);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) t[c] *= rd;
-                        }
-                        uint4* dst = reinterpret_cast<uint4*>(p.o + grow * 64 + 32 * half);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            dst[c] = make_uint4(pack_bf16(t[8 * c], t[8 * c + 1]), pack_bf16(t[8 * c + 2], t[8 * c + 3]),
-                                                pack_bf16(t[8 * c + 4], t[8 * c + 5]), pack_bf16(t[8 * c + 6], t[8 * c + 7]));
+                        dn += p.part_den[grow];
                     }
                 }
+                if (p.part_mode != 1) {
+                    if (kDen) {
+                        if (p.den && half == 0 && valid) p.den[grow] = dn;
+                        const float rd = 1.0f / (dn + p.eps);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) t[c] *= rd;
+                    }
+                    uint32_t o[4][4];   // 16-byte chunks of this row's 64 bytes
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) o[c >> 2][c & 3] = pack_bf16(t[2 * c], t[2 * c + 1]);
+                    // four lanes trade chunks, so that one store writes 64 bytes of 8 rows and not
+                    // 16 bytes of 32: o[r] becomes chunk (lane & 3) of row (lane & ~3) + r
+#pragma unroll
+                    for (int m = 1; m <= 2; m *= 2)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c & m) continue;
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                const bool up = (lane & m) != 0;
+                                const uint32_t give = up ? o[c][w] : o[c + m][w];
+                                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, m);
+                                if (up) o[c][w] = got; else o[c + m][w] = got;
+                            }
+                        }
+                    const int r0 = 32 * q + (lane & ~3);
+                    __nv_bfloat16* dst = p.o + (grow - row + r0) * 64 + 32 * half + 8 * (lane & 3);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (r0 + r < n) *reinterpret_cast<uint4*>(dst + r * 64) = make_uint4(o[r][0], o[r][1], o[r][2], o[r][3]);
+                }
+                if (more) write_y(i + 1);
             }
         }
+        if (kMode == kOutE && lane == 0) bulk_wait<0>();   // this warp's stores have landed
         if (p.last) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -642,7 +854,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     dst[c] = make_float4(run[b][4 * c], run[b][4 * c + 1], run[b][4 * c + 2], run[b][4 * c + 3]);
-                if (b == half && p.has_z && p.last_z) p.last_z[sidx * p.F + f0 + f] = zrun;
+                if (b == half && has_z && p.last_z) p.last_z[sidx * p.F + f0 + f] = zrun;
             }
         }
     }
@@ -659,7 +871,7 @@ __global__ void __launch_bounds__(256) k_dec_seg_scan(float* st, float* sz, cons
                                                       float* last, float* last_z, int F, int nseg, int rev,
                                                       const float* log_decay, const int32_t* lengths, int H, int L)
 {
-    const int64_t bh = blockIdx.y;
+    const int bh = blockIdx.y;
     int x = blockIdx.x * 256 + threadIdx.x;
     int64_t w = static_cast<int64_t>(F) * 64;
     if (x >= w) {
@@ -673,13 +885,13 @@ __global__ void __launch_bounds__(256) k_dec_seg_scan(float* st, float* sz, cons
     const int len = lengths ? min(max(lengths[bh / H], 0), L) : L;
     const int nch = (len + kT - 1) / kT;
     const float g2 = log_decay[bh % H] * kLog2e;
-    float run = first ? first[bh * w + x] : 0.0f;
+    float run = first ? first[bh * w + x] : 0.0f;   // (w is 64 bits wide)
     float* q = st + bh * nseg * w + x;
 #pragma unroll 4
     for (int i = 0; i < nseg; ++i) {
         const int s = rev ? nseg - 1 - i : i;
-        const int lo = static_cast<int>(static_cast<int64_t>(s) * nch / nseg) * kT;
-        const int hi = min(static_cast<int>(static_cast<int64_t>(s + 1) * nch / nseg) * kT, len);
+        const int lo = s * nch / nseg * kT;
+        const int hi = min((s + 1) * nch / nseg * kT, len);
         const float t = q[s * w];
         q[s * w] = run;
         run = fmaf(decay_pow(g2, max(hi - lo, 0)), run, t);
@@ -688,18 +900,19 @@ __global__ void __launch_bounds__(256) k_dec_seg_scan(float* st, float* sz, cons
 }
 
 // [BH][L][cols] bf16 as a 3-D tensor, boxes of 64 columns x 128 tokens, 128-byte swizzle;
-// columns past `cols` and rows past L read as zero.
-bool map_rows(CUtensorMap* m, const void* base, int cols, int L, int64_t BH)
+// columns past `cols` and rows past L read as zero.  out: boxes of 32 columns x 32 tokens,
+// 64-byte swizzle, for stores; what lies past the edges is not written.
+bool map_rows(CUtensorMap* m, const void* base, int cols, int L, int64_t BH, bool out = false)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(L), static_cast<cuuint64_t>(BH)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(L) * cols * 2};
-    const cuuint32_t box[3] = {64, kT, 1};
+    const cuuint32_t box[3] = {out ? 32u : 64u, out ? 32u : static_cast<cuuint32_t>(kT), 1};
     const cuuint32_t es[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_INTERLEAVE_NONE, out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              out ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // How a call is cut: feature blocks of at most 256, and segments of the sequence.
@@ -753,18 +966,28 @@ Carve carve(const DecayArgs& a, const Plan& c, bool bwd, void* ws)
     return k;
 }
 
-template <int kMode>
-cudaError_t launch(const char* name, const CUtensorMap& fs, const CUtensorMap& fq, const CUtensorMap& es,
-                   const CUtensorMap& eq, const P& p, const Plan& c, cudaStream_t st)
+template <int kMode, bool kRev, bool kNorm>
+cudaError_t launch1(const CUtensorMap& fs, const CUtensorMap& fq, const CUtensorMap& es, const CUtensorMap& eq,
+                    const CUtensorMap& out, const P& p, const Plan& c, cudaStream_t st)
 {
     constexpr size_t smem = layout(kMode).total + 1024;
     static_assert(smem <= 232448, "shared memory of one CTA");
-    const cudaError_t e = cudaFuncSetAttribute(k_tc_dec<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const auto kernel = k_tc_dec<kMode, kRev, kNorm>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = c.BH * p.nseg * (kMode == kOutF ? 1 : p.nfb);
-    TraceScope trace_(name, st);
-    k_tc_dec<kMode><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(fs, fq, es, eq, p);
+    kernel<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(fs, fq, es, eq, out, p);
     return cudaGetLastError();
+}
+
+template <int kMode>
+cudaError_t launch(const char* name, const CUtensorMap& fs, const CUtensorMap& fq, const CUtensorMap& es,
+                   const CUtensorMap& eq, const CUtensorMap& out, const P& p, const Plan& c, bool rev, bool norm,
+                   cudaStream_t st)
+{
+    TraceScope trace_(name, st);
+    if (rev) return norm ? launch1<kMode, true, true>(fs, fq, es, eq, out, p, c, st) : launch1<kMode, true, false>(fs, fq, es, eq, out, p, c, st);
+    return norm ? launch1<kMode, false, true>(fs, fq, es, eq, out, p, c, st) : launch1<kMode, false, false>(fs, fq, es, eq, out, p, c, st);
 }
 
 P base(const DecayArgs& a, const Plan& c, int* err)
@@ -778,7 +1001,6 @@ P base(const DecayArgs& a, const Plan& c, int* err)
     p.nseg = c.nseg;
     p.nfb = c.nfb;
     p.fw = c.fw;
-    p.has_z = a.norm;
     p.eps = a.eps;
     p.err = err;
     return p;
@@ -788,7 +1010,7 @@ P base(const DecayArgs& a, const Plan& c, int* err)
 // ready for the output sweeps (the last state written here, or by the sweep that `p.last`
 // is left for when there is one segment).
 cudaError_t segment_states(const DecayArgs& a, const Plan& c, const Carve& k, P& p, const CUtensorMap& fs,
-                           const CUtensorMap& es, const float* first, const float* first_z, float* last,
+                           const CUtensorMap& es, bool rev, const float* first, const float* first_z, float* last,
                            float* last_z, cudaStream_t st)
 {
     p.first = first;
@@ -798,11 +1020,11 @@ cudaError_t segment_states(const DecayArgs& a, const Plan& c, const Carve& k, P&
     q.first = q.first_z = nullptr;
     q.last = k.st;
     q.last_z = k.sz;
-    cudaError_t e = launch<kState>("tc_decay_state", fs, fs, es, es, q, c, st);
+    cudaError_t e = launch<kState>("tc_decay_state", fs, fs, es, es, fs, q, c, rev, a.norm, st);
     if (e != cudaSuccess) return e;
     TraceScope trace_("decay_seg_scan", st);
     k_dec_seg_scan<<<dim3((a.F * 65 + 255) / 256, static_cast<unsigned>(c.BH)), 256, 0, st>>>(
-        k.st, a.norm ? k.sz : nullptr, first, first_z, last, last_z, a.F, c.nseg, p.rev, a.log_decay, a.lengths, a.H, a.L);
+        k.st, a.norm ? k.sz : nullptr, first, first_z, last, last_z, a.F, c.nseg, rev, a.log_decay, a.lengths, a.H, a.L);
     p.first = k.st;
     p.first_z = k.sz;
     return cudaGetLastError();
@@ -811,14 +1033,14 @@ cudaError_t segment_states(const DecayArgs& a, const Plan& c, const Carve& k, P&
 // A sweep whose queries are on the F side: one launch per feature block, the blocks'
 // numerators and denominators added in fp32.
 cudaError_t out_f(const CUtensorMap& fs, const CUtensorMap& fq, const CUtensorMap& es, P p, const Plan& c,
-                  const Carve& k, cudaStream_t st)
+                  const Carve& k, bool rev, bool norm, cudaStream_t st)
 {
     p.part = k.part;
     p.part_den = k.part_den;
     for (int fb = 0; fb < c.nfb; ++fb) {
         p.fb0 = fb;
         p.part_mode = c.nfb == 1 ? 0 : fb == 0 ? 1 : 2;
-        const cudaError_t e = launch<kOutF>("tc_decay_out_f", fs, fq, es, es, p, c, st);
+        const cudaError_t e = launch<kOutF>("tc_decay_out_f", fs, fq, es, es, fs, p, c, rev, norm, st);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -841,49 +1063,48 @@ cudaError_t decay_tc_fwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
     if (!map_rows(&mq, a.phq, a.F, a.L, c.BH) || !map_rows(&mk, a.phk, a.F, a.L, c.BH) || !map_rows(&mv, a.v, 64, a.L, c.BH))
         return cudaErrorInvalidValue;
     P p = base(a, c, err);
-    cudaError_t e = segment_states(a, c, k, p, mk, mv, a.S_in, a.z_in, a.S_out, a.z_out, st);
+    cudaError_t e = segment_states(a, c, k, p, mk, mv, false, a.S_in, a.z_in, a.S_out, a.z_out, st);
     if (e != cudaSuccess) return e;
     if (c.nseg == 1) {
         p.last = a.S_out;
         p.last_z = a.z_out;
     }
-    p.has_den = a.norm;
     p.o = static_cast<__nv_bfloat16*>(a.out_w);
     p.den = a.den_w;
-    return out_f(mk, mq, mv, p, c, k, st);
+    return out_f(mk, mq, mv, p, c, k, false, a.norm, st);
 }
 
 cudaError_t decay_tc_bwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st)
 {
     const Plan c = plan(a);
     const Carve k = carve(a, c, true, ws);
-    CUtensorMap mq, mk, mv, mo;
+    CUtensorMap mq, mk, mv, mo, mdq, mdk;
     if (!map_rows(&mq, a.phq, a.F, a.L, c.BH) || !map_rows(&mk, a.phk, a.F, a.L, c.BH) ||
-        !map_rows(&mv, a.v, 64, a.L, c.BH) || !map_rows(&mo, a.dout, 64, a.L, c.BH))
+        !map_rows(&mv, a.v, 64, a.L, c.BH) || !map_rows(&mo, a.dout, 64, a.L, c.BH) ||
+        !map_rows(&mdq, a.dphq, a.F, a.L, c.BH, true) || !map_rows(&mdk, a.dphk, a.F, a.L, c.BH, true))
         return cudaErrorInvalidValue;
     cudaError_t e = a.norm ? decay_row_stats(a, k.rz, k.r, st) : cudaSuccess;
     if (e != cudaSuccess) return e;
     const float *rz = a.norm ? k.rz : nullptr, *r = a.norm ? k.r : nullptr;
     P s = base(a, c, err);   // dphq from the states before each token
-    if ((e = segment_states(a, c, k, s, mk, mv, a.S_in, a.z_in, nullptr, nullptr, st)) != cudaSuccess) return e;
+    if ((e = segment_states(a, c, k, s, mk, mv, false, a.S_in, a.z_in, nullptr, nullptr, st)) != cudaSuccess) return e;
     s.q_mul = rz;
     s.q_off = r;
     s.o = static_cast<__nv_bfloat16*>(a.dphq);
-    if ((e = launch<kOutE>("tc_decay_out_e", mk, mk, mv, mo, s, c, st)) != cudaSuccess) return e;
+    if ((e = launch<kOutE>("tc_decay_out_e", mk, mk, mv, mo, mdq, s, c, false, a.norm, st)) != cudaSuccess) return e;
     P g = base(a, c, err);   // dphk and dv from the states after each token
-    g.rev = 1;
     g.s_mul = rz;
     g.s_off = r;
-    g.z_delta = a.norm;
-    if ((e = segment_states(a, c, k, g, mq, mo, a.dS_out, a.dz_out, a.dS_in, a.dz_in, st)) != cudaSuccess) return e;
+    if ((e = segment_states(a, c, k, g, mq, mo, true, a.dS_out, a.dz_out, a.dS_in, a.dz_in, st)) != cudaSuccess) return e;
     g.o = static_cast<__nv_bfloat16*>(a.dphk);
-    if ((e = launch<kOutE>("tc_decay_out_e", mq, mq, mo, mv, g, c, st)) != cudaSuccess) return e;
+    if ((e = launch<kOutE>("tc_decay_out_e", mq, mq, mo, mv, mdk, g, c, true, a.norm, st)) != cudaSuccess) return e;
     if (c.nseg == 1) {       // (the sweep that writes over dS_out when dS_in is dS_out: the last one)
         g.last = a.dS_in;
         g.last_z = a.dz_in;
+        g.z_state = a.dz_in != nullptr;
     }
     g.o = static_cast<__nv_bfloat16*>(a.dv);
-    return out_f(mq, mk, mo, g, c, k, st);
+    return out_f(mq, mk, mo, g, c, k, true, a.norm, st);
 }
 
 }  // namespace slay
