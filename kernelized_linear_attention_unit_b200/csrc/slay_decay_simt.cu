@@ -422,20 +422,28 @@ __global__ void __launch_bounds__(kNT) k_dec_out_e(Sweep s, T* o, bool norm)
     }
 }
 
-// Row statistics of the normalized backward: a warp a row, two elements a lane.
+// Row statistics of the normalized backward: 16 bytes a lane, so 8 (bf16) or 16 (fp32) lanes a
+// row; bound by the reads of out and dout.
 template <typename T>
 __global__ void __launch_bounds__(256) k_dec_row_stats(const T* out, const T* dout, const float* den, float* rz,
                                                        float* r, int64_t rows, float eps, const int32_t* lengths,
                                                        int64_t HL, int L)
 {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= rows) return;
-    if (lengths && row % L >= lengths[row / HL]) return;   // rows behind the sequence are never read
-    const T *a = out + row * 64 + 2 * lane, *b = dout + row * 64 + 2 * lane;
-    float d = fmaf(ldf(a), ldf(b), ldf(a + 1) * ldf(b + 1));
-    for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-    if (lane == 0) {
+    constexpr int kE = 16 / sizeof(T), kLanes = 64 / kE;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, row = i / kLanes;
+    // rows behind a sequence are never read by the sweeps, whatever comes out for them
+    const bool in = row < rows && !(lengths && row % L >= lengths[row / HL]);
+    float d = 0.0f;
+    if (in) {
+#pragma unroll
+        for (int e = 0; e < kE; e += 4) {
+            const float4 a = ld4(out + i * kE + e), b = ld4(dout + i * kE + e);
+            d = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, d))));
+        }
+    }
+#pragma unroll
+    for (int x = kLanes / 2; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
+    if (in && i % kLanes == 0) {
         rz[row] = 1.0f / (den[row] + eps);
         r[row] = d;
     }
@@ -575,7 +583,8 @@ cudaError_t bwd_t(const DecayArgs& a, void* ws, cudaStream_t st)
 cudaError_t decay_row_stats(const DecayArgs& a, float* rz, float* r, cudaStream_t st)
 {
     const int64_t rows = static_cast<int64_t>(a.B) * a.H * a.L, HL = static_cast<int64_t>(a.H) * a.L;
-    const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+    const int lanes = a.dt == SLAY_F32 ? 16 : 8;
+    const unsigned grid = static_cast<unsigned>((rows * lanes + 255) / 256);
     TraceScope trace_("simt_decay_row_stats", st);
     if (a.dt == SLAY_F32)
         k_dec_row_stats<float><<<grid, 256, 0, st>>>(static_cast<const float*>(a.out), static_cast<const float*>(a.dout), a.den,

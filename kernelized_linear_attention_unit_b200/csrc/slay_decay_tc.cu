@@ -44,11 +44,16 @@ constexpr int kT = 128;               // tokens per chunk
 constexpr int kTile = kT * 128;       // [128][64] bf16, 128-byte swizzle = 16 KiB
 constexpr int kSlab = 64 * 128;       // [64 f][64 e] bf16 = 8 KiB
 constexpr int kExt = 16 * 128;        // [16][64] bf16 = 2 KiB
-constexpr int kThreads = 32 * 12;     // MMA warp, TMA warp (and two idle ones), 8 epilogue warps
 constexpr int kNumSMs = 148;
 constexpr int kMaxFw = 256;           // features of one sweep
 
 enum Mode { kState = 0, kOutF = 1, kOutE = 2 };
+
+// Warps: 0 issues the MMAs, 1 the TMA loads (2 the query slices'); 4 on are the epilogue.  kOutE, whose
+// outputs are F wide, gives the state four warps of its own beside eight for scores and
+// outputs; elsewhere eight do both (and hold half as much of the state each).
+__host__ __device__ constexpr bool split(int mode) { return mode == kOutE; }
+__host__ __device__ constexpr int threads(int mode) { return 32 * (split(mode) ? 16 : 12); }
 
 // tensor memory columns.  P~ replaces the scores' first 64 columns; an output accumulator
 // takes the other 64.  T of 128 features: the first limb's 64 columns, in the modes with
@@ -61,8 +66,8 @@ __host__ __device__ constexpr uint32_t t_stride(int mode) { return mode == kOutE
 __host__ __device__ constexpr int limb_tiles(int mode) { return mode == kState ? 6 : mode == kOutE ? 2 : 3; }
 
 enum {
-    B_FSF = 0, B_FSE = 4, B_FQF = 8, B_FQE = 10, B_ESF = 12, B_ESE = 14, B_YF = 16, B_MF = 18, B_PF, B_PT, B_TF, B_OD,
-    B_OF = 23, B_OE = 25, B_NUM = 27
+    B_FSF = 0, B_FSE = 4, B_FQF = 8, B_ESF = 12, B_ESE = 14, B_YF = 16, B_MF = 18, B_PF = 20, B_PT, B_OD,
+    B_TF = 23, B_OF = 25, B_OE = 27, B_FQE = 29, B_NUM = 33
 };
 
 struct Layout {
@@ -74,10 +79,10 @@ __host__ __device__ constexpr Layout layout(int mode)
     Layout l{};
     uint32_t o = 0;
     l.fs = o; o += 4 * kTile;                           // ring of four F-side slices
-    l.fq = o; o += mode == kOutF ? 2 * kTile : 0;       // ring of two query slices
-    l.es = o; o += 2 * kTile;                           // 64-wide side, two chunks
+    l.fq = o; o += mode == kOutF ? 3 * kTile : 0;       // ring of query slices: four, or three and
+    l.y = o; o += limb_tiles(mode) * kTile;             // the third of the weighted rows' limbs in that tile
+    l.es = o; o += (mode == kOutF ? 1 : 2) * kTile;     // 64-wide side, two chunks (kOutF: one)
     l.eq = o; o += mode == kOutE ? 2 * kTile : 0;       // 64-wide queries, two chunks
-    l.y = o; o += limb_tiles(mode) * kTile;             // weighted rows in limbs (kState: two chunks)
     l.m = o; o += mode == kState ? 0 : 4 * kSlab;       // the state as an operand
     l.zext = o; o += mode == kOutF ? 4 * kExt : 0;      // its z column, three limbs of 16 columns
     l.wext = o; o += (mode == kState ? 4 : 2) * kExt;   // z weights of the chunk's tokens, likewise
@@ -161,13 +166,15 @@ __device__ __forceinline__ bool elect_one()
 // kRev: the sweep walks the chunks backward.  kNorm: the normalized form, whose backward puts
 // its row scalars on the state tokens (kRev) or on the query tokens (kOutE forward).
 template <int kMode, bool kRev, bool kNorm>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads(kMode), 1)
 k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtensorMap tfq,
          const __grid_constant__ CUtensorMap tes, const __grid_constant__ CUtensorMap teq,
          const __grid_constant__ CUtensorMap tout, const P p)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // (stays a shared address)
+    constexpr bool kSplit = split(kMode);
+    constexpr int kThreads = threads(kMode), kEs = kMode == kOutF ? 1 : 2;
     constexpr bool kCols = kRev && kNorm, kRows = kMode == kOutE && !kRev && kNorm, kDen = kMode == kOutF && !kRev && kNorm;
     constexpr Layout Lo = layout(kMode);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Lo.bar);
@@ -193,6 +200,9 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     const bool has_z = kNorm && (kMode != kOutF || !kRev || p.z_state);
     const int nl = g2 == 0.0f && !kCols ? 1 : (kMode == kState || (kMode == kOutF && p.last)) ? 3 : 2;
 
+    // kOutF: limb tiles 0, 1 at y + 16 KiB, 2 at y, which is the query ring's fourth slot otherwise
+    const int nfq = nl == 3 ? 3 : 4;
+    constexpr uint32_t kY = kMode == kOutF ? Lo.y + kTile : Lo.y;
     if (warp == 0) {
         tmem_alloc(tslot, 512);
         tmem_relinquish();
@@ -204,7 +214,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     if (tid < 32) reinterpret_cast<float*>(sm + Lo.pw)[64 + tid] = decay_pow(g2, kRev ? tid : 31 - tid);
     if (tid == 0) {
         for (int i = 0; i < B_NUM; ++i)
-            mbar_init(&bar[i], i == B_YF || i == B_YF + 1 || i == B_MF || i == B_PT || i == B_OE || i == B_OE + 1 ? 8 : 1);
+            mbar_init(&bar[i], i >= B_YF && i < B_YF + 4 ? (kSplit ? 4 : 8) : i == B_PT || i == B_OE || i == B_OE + 1 ? 8 : 1);
         mbar_fence_init();
         tma_prefetch_desc(&tfs);
         tma_prefetch_desc(&tes);
@@ -224,18 +234,22 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     // waits on the k-th completion (k >= 0) of a barrier
     auto wait_k = [&](int b, int k) { wt.wait(&bar[b], static_cast<uint32_t>(k & 1)); };
 
-    // Registers: 384 threads launch with 168 each; the loading warpgroup gives some of its share
-    // to the epilogue, which holds the state: 88 + 2 x 208 = 3 x 168.
+    // Registers: the loading warpgroup gives some of its share to the warps that hold the
+    // state.  384 threads launch with 168 each: 88 + 2 x 208 = 3 x 168; 512 with 128:
+    // 64 + 192 + 2 x 128 = 4 x 128.
     if (warp < 4) {
-        regs_dec<88>();
+        regs_dec<kSplit ? 64 : 88>();
         if (warp == 1 && lane == 0) {
             // -------------------------------------------------------------- TMA loads
             for (int i = 0; i < count && wt.ok; ++i) {
-                const int t0 = chunk_of(i) * kT, b = i & 1;
-                if (i >= 2) wait_k(B_ESE + b, (i >> 1) - 1);
-                mbar_arrive_expect_tx(&bar[B_ESF + b], kMode == kOutE ? 2 * kTile : kTile);
-                tma_load_3d(sm + Lo.es + b * kTile, &tes, &bar[B_ESF + b], 0, t0, bh);
-                if (kMode == kOutE) tma_load_3d(sm + Lo.eq + b * kTile, &teq, &bar[B_ESF + b], 0, t0, bh);
+                const int t0 = chunk_of(i) * kT, b = i % kEs;
+                auto load_e = [&] {   // the 64-wide rows
+                    if (i >= kEs) wait_k(B_ESE + b, i / kEs - 1);
+                    mbar_arrive_expect_tx(&bar[B_ESF + b], kMode == kOutE ? 2 * kTile : kTile);
+                    tma_load_3d(sm + Lo.es + b * kTile, &tes, &bar[B_ESF + b], 0, t0, bh);
+                    if (kMode == kOutE) tma_load_3d(sm + Lo.eq + b * kTile, &teq, &bar[B_ESF + b], 0, t0, bh);
+                };
+                if (kMode != kOutF || i == 0) load_e();
                 for (int s = 0; s < nsE; ++s) {
                     const int u = i * nsE + s, sl = u & 3;
                     if (u >= 4) wait_k(B_FSE + sl, (u >> 2) - 1);
@@ -245,11 +259,19 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                     } else {
                         mbar_arrive(&bar[B_FSF + sl]);   // the second half of the last pair: not read
                     }
-                    if (kMode == kOutF && s < ns) {
-                        const int u2 = i * ns + s, q = u2 & 1;
-                        if (u2 >= 2) wait_k(B_FQE + q, (u2 >> 1) - 1);
-                        mbar_arrive_expect_tx(&bar[B_FQF + q], kTile);
-                        tma_load_3d(sm + Lo.fq + q * kTile, &tfq, &bar[B_FQF + q], f0 + 64 * s, t0, bh);
+                }
+                if (kMode == kOutF && i > 0) load_e();   // its one buffer is freed after the slices'
+            }
+        } else if (kMode == kOutF && warp == 2 && lane == 0) {
+            int fq = 0, fqr = 0;   // query slot, its use
+            for (int i = 0; i < count && wt.ok; ++i) {
+                for (int s = 0; s < ns; ++s) {
+                    if (fqr >= 1) wait_k(B_FQE + fq, fqr - 1);
+                    mbar_arrive_expect_tx(&bar[B_FQF + fq], kTile);
+                    tma_load_3d(sm + Lo.fq + fq * kTile, &tfq, &bar[B_FQF + fq], f0 + 64 * s, chunk_of(i) * kT, bh);
+                    if (++fq == nfq) {
+                        fq = 0;
+                        ++fqr;
                     }
                 }
             }
@@ -265,14 +287,15 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
             constexpr uint32_t kTd = kTile >> 4, kSd = kSlab >> 4, kEd = kExt >> 4;
             const uint64_t d0 = sdesc(sbase, 16, 1024, kLayoutSW128);
             const uint64_t dT = sdesc(sbase, kTile, 1024, kLayoutSW128);   // the next 64 rows or columns one tile on
-            constexpr uint32_t oFs = Lo.fs >> 4, oFq = Lo.fq >> 4, oEs = Lo.es >> 4, oEq = Lo.eq >> 4, oY = Lo.y >> 4,
+            constexpr uint32_t oFs = Lo.fs >> 4, oFq = Lo.fq >> 4, oEs = Lo.es >> 4, oEq = Lo.eq >> 4, oY = kY >> 4,
                                oM = Lo.m >> 4, oZe = Lo.zext >> 4, oWe = Lo.wext >> 4;
             auto wait_m = [&](int b, int k) {
                 wait_k(b, k);
                 tc_fence_after();
             };
+            int fq = 0, fqr = 0;   // query slot, its use
             for (int i = 0; i < count && wt.ok; ++i) {
-                const int t0 = chunk_of(i) * kT, n = min(kT, len - t0), eb = i & 1;
+                const int t0 = chunk_of(i) * kT, n = min(kT, len - t0), eb = i % kEs;
                 // rows of the tensor behind this sequence may hold anything: cleared in the
                 // tiles, since they enter sums over tokens (rows past L arrive as zero)
                 const bool clear = n < kT && t0 + n < p.L;
@@ -300,7 +323,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                     for (; l < nl; ++l)
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            umma_bf16(t, da + 128 * kk, d0 + oy + l * kTd + 128 * kk, idMM, (l > 0 || kk > 0) ? 1u : 0u);
+                            umma_bf16(t, da + 128 * kk, d0 + (kMode == kOutF && l == 2 ? Lo.y >> 4 : oy + l * kTd) + 128 * kk, idMM, (l > 0 || kk > 0) ? 1u : 0u);
                     if (has_z) {
                         const uint64_t dw = d0 + oWe + (kMode == kState ? eb * 2 * kEd : 0);
 #pragma unroll
@@ -318,9 +341,9 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                     // the scores and the state's part take the place of the last chunk's outputs
                     if (i >= 1) wait_m(B_OE, i - 1);
                     for (int s = 0; s < ns; ++s) {
-                        const int sl = slice(s), u2 = i * ns + s, q = u2 & 1;
-                        wait_m(B_FQF + q, u2 >> 1);
-                        const uint64_t dx = d0 + oFq + q * kTd, dyy = d0 + oFs + sl * kTd;
+                        const int sl = slice(s);
+                        wait_m(B_FQF + fq, fqr);
+                        const uint64_t dx = d0 + oFq + fq * kTd, dyy = d0 + oFs + sl * kTd;
                         if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
@@ -338,7 +361,11 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                                 for (int kk = 0; kk < 4; ++kk)
                                     umma_bf16(tmem + kColDen, dx + 2 * kk, d0 + oZe + s * kEd + 2 * kk, idKz,
                                               (s > 0 || kk > 0) ? 1u : 0u);
-                            umma_commit(&bar[B_FQE + q]);
+                            umma_commit(&bar[B_FQE + fq]);
+                        }
+                        if (++fq == nfq) {
+                            fq = 0;
+                            ++fqr;
                         }
                     }
                     wait_m(B_YF, i);
@@ -358,7 +385,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                         umma_commit(&bar[B_ESE + eb]);
                     }
                 } else if (kMode == kOutE) {
-                    wait_m(B_ESF + eb, i >> 1);
+                    wait_m(B_ESF + eb, i / kEs);
                     if (clear) clear_rows(Lo.es + eb * kTile);
                     const int v1 = i * ns - 1, vo = (v1 & 1) ? v1 : v1 - 1;   // last use of the buffer over P
                     if (vo >= 1) wait_m(B_OE + 1, vo >> 1);
@@ -403,19 +430,17 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                     }
                 } else {
                     wait_m(B_YF + eb, i >> 1);
-                    wait_m(B_MF, i);
-                    for (int s = 0; s < ns; s += 2) {
+                    for (int s = 0; s < ns; s += 2) {   // a pair's T is read while the other's is summed
                         slice(s);
                         if (s + 1 < ns) slice(s + 1);
+                        wait_m(B_MF + (s >> 1), i);
                         if (elect_one()) {
                             state_pair(s);
                             free_pair(s);
+                            umma_commit(&bar[B_TF + (s >> 1)]);
                         }
                     }
-                    if (elect_one()) {
-                        umma_commit(&bar[B_TF]);
-                        umma_commit(&bar[B_ESE + eb]);
-                    }
+                    if (elect_one()) umma_commit(&bar[B_ESE + eb]);
                 }
                 __syncwarp();
             }
@@ -424,8 +449,8 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     } else {
         // ------------------------------------------------------------------ epilogue
         // (no early exit on a wait that ran out: the pairs of warps share named barriers)
-        regs_inc<208>();
-        const int q = warp & 3, ew = warp - 4, half = ew >> 2;
+        const int q = warp & 3, ew = warp - (kSplit ? 8 : 4), half = kSplit && warp < 8 ? 0 : ew >> 2;
+        constexpr int kW = kSplit ? 64 : 32;   // columns of M a state thread holds
         const int row = 32 * q + lane;   // token of scores, outputs and weighted rows; feature of T
         const uint32_t trow = tmem + ((32u * q) << 16);
         const float* pw = reinterpret_cast<const float*>(sm + Lo.pw);
@@ -434,147 +459,6 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
         float* dsum = reinterpret_cast<float*>(sm + Lo.dsum);
         float* zf = reinterpret_cast<float*>(sm + Lo.zf);
         const int64_t sidx = static_cast<int64_t>(bh) * p.nseg + seg;
-        float run[2][32], zrun = 0.0f;   // M at (f = 128 b + row, e = 32 half + c); z at b = half
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int f = 128 * b + row;
-            const bool in = p.first && f < fv;
-            const float4* src = reinterpret_cast<const float4*>(p.first + ((sidx * p.F) + f0 + f) * 64 + 32 * half);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float4 w = in ? src[c] : make_float4(0.f, 0.f, 0.f, 0.f);
-                run[b][4 * c] = w.x;
-                run[b][4 * c + 1] = w.y;
-                run[b][4 * c + 2] = w.z;
-                run[b][4 * c + 3] = w.w;
-            }
-            if (b == half && in && has_z) zrun = p.first_z[sidx * p.F + f0 + f];
-        }
-        // the operand copy of M, and its z column, for chunk i
-        auto write_m = [&](int i) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int f = 128 * b + row;
-                if (f < 64 * ns) {
-                    const uint32_t slab = sbase + Lo.m + (f >> 6) * kSlab;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        st_shared_v4(slab + sw128_off(f & 63, 4 * half + c),
-                                     pack_bf16(run[b][8 * c], run[b][8 * c + 1]), pack_bf16(run[b][8 * c + 2], run[b][8 * c + 3]),
-                                     pack_bf16(run[b][8 * c + 4], run[b][8 * c + 5]), pack_bf16(run[b][8 * c + 6], run[b][8 * c + 7]));
-                    if (b == half && has_z) {
-                        if (kMode == kOutF) {
-                            uint16_t l[3];
-                            limbs3(zrun, l);
-                            const uint32_t t = sbase + Lo.zext + (f >> 6) * kExt;
-#pragma unroll
-                            for (int k = 0; k < 3; ++k) st_shared_u16(t + sw128_off(k, (f & 63) >> 3) + (f & 7) * 2, l[k]);
-                        } else {
-                            zf[(i & 1) * kMaxFw + f] = zrun;
-                        }
-                    }
-                }
-            }
-            fence_async_smem();
-            warp_arrive(&bar[B_MF]);
-        };
-        // the weighted rows of chunk i (this thread: token `row`, 32 of its columns) in limbs,
-        // the z weights and the score scalars of its tokens
-        auto write_y = [&](int i) {
-            const int t0 = chunk_of(i) * kT, n = min(kT, len - t0), eb = i & 1;
-            const bool in = row < n;
-            const int64_t grow = static_cast<int64_t>(bh) * p.L + t0 + row;
-            const float mul = kCols && in ? p.s_mul[grow] : 1.0f;
-            const float off = kCols && in ? p.s_off[grow] : 0.0f;
-            const float w = in ? decay_pow(g2, kRev ? row + 1 : n - 1 - row) : 0.0f;
-            const float a = w * mul;
-            const uint32_t ybase = sbase + Lo.y + (kMode == kState ? eb * 3 * kTile : 0);
-            wait_k(B_ESF + eb, i >> 1);
-            uint4 r[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                r[c] = *reinterpret_cast<const uint4*>(sm + Lo.es + eb * kTile + sw128_off(row, 4 * half + c));
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t o = sw128_off(row, 4 * half + c);
-                uint32_t v[4] = {r[c].x, r[c].y, r[c].z, r[c].w};
-                if (!in) {
-                    v[0] = v[1] = v[2] = v[3] = 0u;
-                    if (kMode == kOutF) st_shared_v4(sbase + Lo.es + eb * kTile + o, 0u, 0u, 0u, 0u);   // an operand itself
-                }
-                if (nl == 1) {
-                    st_shared_v4(ybase + o, v[0], v[1], v[2], v[3]);
-                    continue;
-                }
-                float2 y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = fmul2(make_float2(a, a), make_float2(bf_lo(v[e]), bf_hi(v[e])));
-#pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    if (k >= nl) break;
-                    uint32_t l[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        l[e] = pack_bf16(y[e].x, y[e].y);
-                        y[e] = ffma2(make_float2(-1.0f, -1.0f), make_float2(bf_lo(l[e]), bf_hi(l[e])), y[e]);
-                    }
-                    st_shared_v4(ybase + k * kTile + o, l[0], l[1], l[2], l[3]);
-                }
-            }
-            if (half == 0) {
-                if (has_z) {
-                    uint16_t l[3];
-                    limbs3(kCols ? -a * off : w, l);
-                    const uint32_t t = sbase + Lo.wext + (kMode == kState ? eb * 2 * kExt : 0) + (row >> 6) * kExt;
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) st_shared_u16(t + sw128_off(k, (row & 63) >> 3) + (row & 7) * 2, l[k]);
-                }
-                if (kCols) {
-                    smul[(i & 1) * kT + row] = mul;
-                    soff[(i & 1) * kT + row] = off;
-                }
-            }
-            fence_async_smem();
-            warp_arrive(&bar[kMode == kState ? B_YF + eb : B_YF]);
-        };
-        // M <- lambda^n M + T
-        auto update_m = [&](int i) {
-            const int n = min(kT, len - chunk_of(i) * kT);
-            const float lam = decay_pow(g2, n);
-            const bool two = kMode != kOutE && nl > 1;
-            wait_k(B_TF, i);
-            tc_fence_after();
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (2 * b >= ns) break;
-                const uint32_t tc = trow + col_t(kMode) + t_stride(kMode) * b;
-                uint32_t t[32], t2[32], z0 = 0, z1 = 0, z2 = 0;
-                tmem_ld32(tc + 32 * half, t);
-                if (two) tmem_ld32(tc + 64 + 32 * half, t2);
-                if (has_z && b == half) {
-                    tmem_ld1(tc + col_z(kMode), z0);
-                    tmem_ld1(tc + col_z(kMode) + 1, z1);
-                    tmem_ld1(tc + col_z(kMode) + 2, z2);
-                }
-                tmem_wait_ld();
-                reg_fence(t);
-                reg_fence(t2);
-                reg_fence1(z0);
-                reg_fence1(z1);
-                reg_fence1(z2);
-#pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    float2 w = make_float2(__uint_as_float(t[c]), __uint_as_float(t[c + 1]));
-                    if (two) w = fadd2(w, make_float2(__uint_as_float(t2[c]), __uint_as_float(t2[c + 1])));
-                    const float2 r = ffma2(make_float2(lam, lam), make_float2(run[b][c], run[b][c + 1]), w);
-                    run[b][c] = r.x;
-                    run[b][c + 1] = r.y;
-                }
-                if (has_z && b == half)
-                    zrun = fmaf(lam, zrun, __uint_as_float(z0) + (__uint_as_float(z1) + __uint_as_float(z2)));
-            }
-            tc_fence_before();
-        };
         // the scalars of four query / state tokens: off the raw scores, onto the weights
         auto scale = [&](int par, int j, float2 off, float2& s0, float2& s1, float2& w0, float2& w1) {
             if (kRows) {
@@ -675,11 +559,249 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) tmem_st16(trow + kColP + 16 * (half + 2 * hh), pk[hh]);
             tmem_wait_st();
+            // (before PT: no barrier may run two phases ahead of a thread that waits on it)
+            if (kMode == kOutE && has_z) wait_k(B_MF, i);   // zf of this chunk
             tc_fence_before();
             warp_arrive(&bar[B_PT]);
         };
+        // a chunk's F-wide outputs
+        auto out_e = [&](int i) {
+            const int t0 = chunk_of(i) * kT, n = min(kT, len - t0), par = i & 1;
+            const int64_t grow = static_cast<int64_t>(bh) * p.L + t0 + row;
+            const bool valid = row < n;
+            const float fac = decay_pow(g2, kRev ? max(n - 1 - row, 0) : row + 1);
+            float qo = 0.0f, qm = 1.0f;
+            if (kRows && valid) {
+                qm = p.q_mul[grow];
+                qo = p.q_off[grow];
+            }
+            scores(i, qo, qm);
+            // outputs, 64 features at a time; through the warp's staging box and a TMA store
+            // unless rows of the tensor behind the sequence have to stay
+            const float fq = fac * qm, zc = kRows ? -qo : 1.0f;
+            const bool whole = n == kT || t0 + n == p.L;
+            const uint32_t box = sbase + Lo.stg + ew * 2048;
+            for (int s = 0; s < ns; ++s) {
+                const int v = i * ns + s, ob = v & 1;
+                wait_k(B_OF + ob, v >> 1);
+                tc_fence_after();
+                uint32_t a[32], e[32];
+                tmem_ld32(trow + (ob ? kColOi : kColOi0) + 32 * half, a);
+                tmem_ld32(trow + (ob ? kColOe1 : kColOe0) + 32 * half, e);
+                tmem_wait_ld();
+                reg_fence(a);
+                reg_fence(e);
+                tc_fence_before();
+                warp_arrive(&bar[B_OE + ob]);
+                const int fl = 64 * s + 32 * half;
+                if (has_z) {
+                    const float4* z4 = reinterpret_cast<const float4*>(zf + par * kMaxFw + fl);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float4 z = z4[c];
+                        e[4 * c] = __float_as_uint(fmaf(zc, z.x, __uint_as_float(e[4 * c])));
+                        e[4 * c + 1] = __float_as_uint(fmaf(zc, z.y, __uint_as_float(e[4 * c + 1])));
+                        e[4 * c + 2] = __float_as_uint(fmaf(zc, z.z, __uint_as_float(e[4 * c + 2])));
+                        e[4 * c + 3] = __float_as_uint(fmaf(zc, z.w, __uint_as_float(e[4 * c + 3])));
+                    }
+                }
+                uint32_t o[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    o[c] = pack_bf16(fmaf(fq, __uint_as_float(e[2 * c]), __uint_as_float(a[2 * c])),
+                                     fmaf(fq, __uint_as_float(e[2 * c + 1]), __uint_as_float(a[2 * c + 1])));
+                if (whole) {
+                    if (lane == 0) bulk_wait_read<0>();   // the box's last store has read it
+                    __syncwarp();
+                    const uint32_t rsw = (static_cast<uint32_t>(lane) >> 1) & 3u;   // 64-byte swizzle
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        st_shared_v4(box + lane * 64u + ((static_cast<uint32_t>(c) ^ rsw) << 4), o[4 * c], o[4 * c + 1],
+                                     o[4 * c + 2], o[4 * c + 3]);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && fl < fv) {
+                        tma_store_3d(&tout, sm + Lo.stg + ew * 2048, f0 + fl, t0 + 32 * q, bh);
+                        bulk_commit_group();
+                    }
+                } else if (valid) {
+                    __nv_bfloat16* dst = p.o + grow * p.F + f0 + fl;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (fl + 8 * c < fv)
+                            *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                }
+            }
+        };
+        if (kSplit && warp >= 8) {
+            for (int i = 0; i < count; ++i) out_e(i);
+            if (lane == 0) bulk_wait<0>();   // this warp's stores have landed
+        } else {
+        regs_inc<kSplit ? 192 : 208>();
+        float run[2][kW], zrun[2] = {0.0f, 0.0f};   // M at (f = 128 b + row, e = 32 half + c); z at b
+        auto has_zrow = [&](int b) { return has_z && (kSplit || b == half); };
+        {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int f = 128 * b + row;
+                const bool in = p.first && f < fv;
+                const float4* src = reinterpret_cast<const float4*>(p.first + ((sidx * p.F) + f0 + f) * 64 + 32 * half);
+#pragma unroll
+                for (int c = 0; c < kW / 4; ++c) {
+                    const float4 w = in ? src[c] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    run[b][4 * c] = w.x;
+                    run[b][4 * c + 1] = w.y;
+                    run[b][4 * c + 2] = w.z;
+                    run[b][4 * c + 3] = w.w;
+                }
+                if (in && has_zrow(b)) zrun[b] = p.first_z[sidx * p.F + f0 + f];
+            }
+        }
+        // the operand copy of M, and its z column, for chunk i
+        auto write_m = [&](int i) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int f = 128 * b + row;
+                if (f < 64 * ns) {
+                    const uint32_t slab = sbase + Lo.m + (f >> 6) * kSlab;
+#pragma unroll
+                    for (int c = 0; c < kW / 8; ++c)
+                        st_shared_v4(slab + sw128_off(f & 63, 4 * half + c),
+                                     pack_bf16(run[b][8 * c], run[b][8 * c + 1]), pack_bf16(run[b][8 * c + 2], run[b][8 * c + 3]),
+                                     pack_bf16(run[b][8 * c + 4], run[b][8 * c + 5]), pack_bf16(run[b][8 * c + 6], run[b][8 * c + 7]));
+                    if (has_zrow(b)) {
+                        if (kMode == kOutF) {
+                            uint16_t l[3];
+                            limbs3(zrun[b], l);
+                            const uint32_t t = sbase + Lo.zext + (f >> 6) * kExt;
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) st_shared_u16(t + sw128_off(k, (f & 63) >> 3) + (f & 7) * 2, l[k]);
+                        } else {
+                            zf[(i & 1) * kMaxFw + f] = zrun[b];
+                        }
+                    }
+                }
+            }
+            fence_async_smem();
+            warp_arrive(&bar[B_MF]);
+        };
+        // the weighted rows of chunk i (this thread: token `row`, 32 of its columns) in limbs,
+        // the z weights and the score scalars of its tokens
+        auto write_y = [&](int i) {
+            const int t0 = chunk_of(i) * kT, n = min(kT, len - t0), eb = i % kEs;
+            const bool in = row < n;
+            const int64_t grow = static_cast<int64_t>(bh) * p.L + t0 + row;
+            const float mul = kCols && in ? p.s_mul[grow] : 1.0f;
+            const float off = kCols && in ? p.s_off[grow] : 0.0f;
+            const float w = in ? decay_pow(g2, kRev ? row + 1 : n - 1 - row) : 0.0f;
+            const float a = w * mul;
+            const uint32_t ybase = sbase + kY + (kMode == kState ? eb * 3 * kTile : 0);
+            wait_k(B_ESF + eb, i / kEs);
+            uint4 r[kW / 8];
+#pragma unroll
+            for (int c = 0; c < kW / 8; ++c)
+                r[c] = *reinterpret_cast<const uint4*>(sm + Lo.es + eb * kTile + sw128_off(row, 4 * half + c));
+#pragma unroll
+            for (int c = 0; c < kW / 8; ++c) {
+                const uint32_t o = sw128_off(row, 4 * half + c);
+                uint32_t v[4] = {r[c].x, r[c].y, r[c].z, r[c].w};
+                if (!in) {
+                    v[0] = v[1] = v[2] = v[3] = 0u;
+                    if (kMode == kOutF) st_shared_v4(sbase + Lo.es + eb * kTile + o, 0u, 0u, 0u, 0u);   // an operand itself
+                }
+                if (nl == 1) {
+                    st_shared_v4(ybase + o, v[0], v[1], v[2], v[3]);
+                    continue;
+                }
+                float2 y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = fmul2(make_float2(a, a), make_float2(bf_lo(v[e]), bf_hi(v[e])));
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    if (k >= (kMode == kOutE ? 2 : nl)) break;
+                    uint32_t l[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        l[e] = pack_bf16(y[e].x, y[e].y);
+                        y[e] = ffma2(make_float2(-1.0f, -1.0f), make_float2(bf_lo(l[e]), bf_hi(l[e])), y[e]);
+                    }
+                    st_shared_v4((kMode == kOutF && k == 2 ? sbase + Lo.y : ybase + k * kTile) + o, l[0], l[1], l[2], l[3]);
+                }
+            }
+            if (half == 0) {
+                if (has_z) {
+                    uint16_t l[3];
+                    limbs3(kCols ? -a * off : w, l);
+                    const uint32_t t = sbase + Lo.wext + (kMode == kState ? eb * 2 * kExt : 0) + (row >> 6) * kExt;
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) st_shared_u16(t + sw128_off(k, (row & 63) >> 3) + (row & 7) * 2, l[k]);
+                }
+                if (kCols) {
+                    smul[(i & 1) * kT + row] = mul;
+                    soff[(i & 1) * kT + row] = off;
+                }
+            }
+            fence_async_smem();
+            warp_arrive(&bar[kMode == kState ? B_YF + eb : B_YF]);
+        };
+        // M <- lambda^n M + T
+        auto update_m = [&](int i) {
+            const int n = min(kT, len - chunk_of(i) * kT);
+            const float lam = decay_pow(g2, n);
+            const bool two = kMode != kOutE && nl > 1;
+            if (kMode != kState) {
+                wait_k(B_TF, i);
+                tc_fence_after();
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if (2 * b >= ns) break;
+                if (kMode == kState) {
+                    wait_k(B_TF + b, i);
+                    tc_fence_after();
+                }
+                const uint32_t tc = trow + col_t(kMode) + t_stride(kMode) * b;
+#pragma unroll
+                for (int hh = 0; hh < kW / 32; ++hh) {
+                uint32_t t[32], t2[32], z0 = 0, z1 = 0, z2 = 0;
+                tmem_ld32(tc + 32 * (half + hh), t);
+                if (two) tmem_ld32(tc + 64 + 32 * half, t2);
+                if (hh == 0 && has_zrow(b)) {
+                    tmem_ld1(tc + col_z(kMode), z0);
+                    tmem_ld1(tc + col_z(kMode) + 1, z1);
+                    tmem_ld1(tc + col_z(kMode) + 2, z2);
+                }
+                tmem_wait_ld();
+                reg_fence(t);
+                reg_fence(t2);
+                reg_fence1(z0);
+                reg_fence1(z1);
+                reg_fence1(z2);
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    float2 w = make_float2(__uint_as_float(t[c]), __uint_as_float(t[c + 1]));
+                    if (two) w = fadd2(w, make_float2(__uint_as_float(t2[c]), __uint_as_float(t2[c + 1])));
+                    const float2 r = ffma2(make_float2(lam, lam), make_float2(run[b][32 * hh + c], run[b][32 * hh + c + 1]), w);
+                    run[b][32 * hh + c] = r.x;
+                    run[b][32 * hh + c + 1] = r.y;
+                }
+                if (hh == 0 && has_zrow(b))
+                    zrun[b] = fmaf(lam, zrun[b], __uint_as_float(z0) + (__uint_as_float(z1) + __uint_as_float(z2)));
+                }
+                if (kMode == kState) {
+                    tc_fence_before();
+                    warp_arrive(&bar[B_MF + b]);   // T has been read
+                }
+            }
+            tc_fence_before();
+        };
         if (count > 0) {
-            if (kMode != kState) write_m(0); else warp_arrive(&bar[B_MF]);
+            if (kMode != kState) {
+                write_m(0);
+            } else {
+                warp_arrive(&bar[B_MF]);
+                warp_arrive(&bar[B_MF + 1]);
+            }
             write_y(0);
         }
         for (int i = 0; i < count; ++i) {
@@ -687,84 +809,20 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
             if (kMode == kState) {
                 if (more) write_y(i + 1);   // the other limb buffer: off the state's chain
                 update_m(i);
-                if (more) warp_arrive(&bar[B_MF]);   // T has been read
-                continue;
-            }
-            const int t0 = chunk_of(i) * kT, n = min(kT, len - t0), par = i & 1;
-            const int64_t grow = static_cast<int64_t>(bh) * p.L + t0 + row;
-            const bool valid = row < n;
-            const float fac = decay_pow(g2, kRev ? max(n - 1 - row, 0) : row + 1);
-            if (kMode == kOutE) {
-                float qo = 0.0f, qm = 1.0f;
-                if (kRows && valid) {
-                    qm = p.q_mul[grow];
-                    qo = p.q_off[grow];
-                }
-                scores(i, qo, qm);
-                // outputs, 64 features at a time; through the warp's staging box and a TMA store
-                // unless rows of the tensor behind the sequence have to stay
-                const float fq = fac * qm, zc = kRows ? -qo : 1.0f;
-                const bool whole = n == kT || t0 + n == p.L;
-                const uint32_t box = sbase + Lo.stg + ew * 2048;
-                if (has_z) wait_k(B_MF, i);   // zf of this chunk
-                for (int s = 0; s < ns; ++s) {
-                    const int v = i * ns + s, ob = v & 1;
-                    wait_k(B_OF + ob, v >> 1);
-                    tc_fence_after();
-                    uint32_t a[32], e[32];
-                    tmem_ld32(trow + (ob ? kColOi : kColOi0) + 32 * half, a);
-                    tmem_ld32(trow + (ob ? kColOe1 : kColOe0) + 32 * half, e);
-                    tmem_wait_ld();
-                    reg_fence(a);
-                    reg_fence(e);
-                    tc_fence_before();
-                    warp_arrive(&bar[B_OE + ob]);
-                    const int fl = 64 * s + 32 * half;
-                    if (has_z) {
-                        const float4* z4 = reinterpret_cast<const float4*>(zf + par * kMaxFw + fl);
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const float4 z = z4[c];
-                            e[4 * c] = __float_as_uint(fmaf(zc, z.x, __uint_as_float(e[4 * c])));
-                            e[4 * c + 1] = __float_as_uint(fmaf(zc, z.y, __uint_as_float(e[4 * c + 1])));
-                            e[4 * c + 2] = __float_as_uint(fmaf(zc, z.z, __uint_as_float(e[4 * c + 2])));
-                            e[4 * c + 3] = __float_as_uint(fmaf(zc, z.w, __uint_as_float(e[4 * c + 3])));
-                        }
-                    }
-                    uint32_t o[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        o[c] = pack_bf16(fmaf(fq, __uint_as_float(e[2 * c]), __uint_as_float(a[2 * c])),
-                                         fmaf(fq, __uint_as_float(e[2 * c + 1]), __uint_as_float(a[2 * c + 1])));
-                    if (whole) {
-                        if (lane == 0) bulk_wait_read<0>();   // the box's last store has read it
-                        __syncwarp();
-                        const uint32_t rsw = (static_cast<uint32_t>(lane) >> 1) & 3u;   // 64-byte swizzle
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            st_shared_v4(box + lane * 64u + ((static_cast<uint32_t>(c) ^ rsw) << 4), o[4 * c], o[4 * c + 1],
-                                         o[4 * c + 2], o[4 * c + 3]);
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0 && fl < fv) {
-                            tma_store_3d(&tout, sm + Lo.stg + ew * 2048, f0 + fl, t0 + 32 * q, bh);
-                            bulk_commit_group();
-                        }
-                    } else if (valid) {
-                        __nv_bfloat16* dst = p.o + grow * p.F + f0 + fl;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (fl + 8 * c < fv)
-                                *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-                    }
-                }
+            } else if (kSplit) {
                 update_m(i);
                 if (more) {
+                    // the output warps have passed their wait for this chunk's scalars
+                    if (kCols) wait_k(B_PT, i);
+                    write_y(i + 1);
                     wait_k(B_OD, i);   // the state's operand is read until the chunk's last output
                     write_m(i + 1);
-                    write_y(i + 1);
                 }
             } else {
+                const int t0 = chunk_of(i) * kT, n = min(kT, len - t0), par = i & 1;
+                const int64_t grow = static_cast<int64_t>(bh) * p.L + t0 + row;
+                const bool valid = row < n;
+                const float fac = decay_pow(g2, kRev ? max(n - 1 - row, 0) : row + 1);
                 scores(i, 0.0f, 1.0f);
                 update_m(i);
                 if (more) write_m(i + 1);   // the next chunk's products want the state first
@@ -844,7 +902,6 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 if (more) write_y(i + 1);
             }
         }
-        if (kMode == kOutE && lane == 0) bulk_wait<0>();   // this warp's stores have landed
         if (p.last) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -852,10 +909,11 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 if (f >= fv) continue;
                 float4* dst = reinterpret_cast<float4*>(p.last + ((sidx * p.F) + f0 + f) * 64 + 32 * half);
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
+                for (int c = 0; c < kW / 4; ++c)
                     dst[c] = make_float4(run[b][4 * c], run[b][4 * c + 1], run[b][4 * c + 2], run[b][4 * c + 3]);
-                if (b == half && has_z && p.last_z) p.last_z[sidx * p.F + f0 + f] = zrun;
+                if (has_zrow(b) && p.last_z) p.last_z[sidx * p.F + f0 + f] = zrun[b];
             }
+        }
         }
     }
     wt.report(p.err);
@@ -865,38 +923,51 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Segment sums -> the states entering the segments, in place, S and z in one launch; first
-// and last as in k_dec_scan.  grid (ceil(F * 65 / 256), BH)
+// Segment sums -> the states entering the segments, in place, S and z in one launch, four
+// elements a thread; first and last as in k_dec_scan.  Loads run eight segments ahead of the
+// stores (L2 latency would be paid per segment otherwise).  grid (ceil(F * 65 / 1024), BH)
 __global__ void __launch_bounds__(256) k_dec_seg_scan(float* st, float* sz, const float* first, const float* first_z,
-                                                      float* last, float* last_z, int F, int nseg, int rev,
+                                                      float* last, float* last_z, int F, int nseg, bool rev,
                                                       const float* log_decay, const int32_t* lengths, int H, int L)
 {
+    __shared__ float lam[kNumSMs];
     const int bh = blockIdx.y;
-    int x = blockIdx.x * 256 + threadIdx.x;
+    {
+        const int len = lengths ? min(max(lengths[bh / H], 0), L) : L;
+        const int nch = (len + kT - 1) / kT;
+        const float g2 = log_decay[bh % H] * kLog2e;
+        for (int s = threadIdx.x; s < nseg; s += 256)
+            lam[s] = decay_pow(g2, max(min((s + 1) * nch / nseg * kT, len) - s * nch / nseg * kT, 0));
+    }
+    __syncthreads();
+    int x = (blockIdx.x * 256 + threadIdx.x) * 4;
     int64_t w = static_cast<int64_t>(F) * 64;
     if (x >= w) {
-        if (!sz || x >= w + F) return;
         x -= static_cast<int>(w);
         w = F;
+        if (!sz || x >= F) return;   // (F % 8 == 0: whole float4s)
         st = sz;
         first = first_z;
         last = last_z;
     }
-    const int len = lengths ? min(max(lengths[bh / H], 0), L) : L;
-    const int nch = (len + kT - 1) / kT;
-    const float g2 = log_decay[bh % H] * kLog2e;
-    float run = first ? first[bh * w + x] : 0.0f;   // (w is 64 bits wide)
+    float4 run = first ? *reinterpret_cast<const float4*>(first + bh * w + x) : make_float4(0.f, 0.f, 0.f, 0.f);
     float* q = st + bh * nseg * w + x;
-#pragma unroll 4
-    for (int i = 0; i < nseg; ++i) {
-        const int s = rev ? nseg - 1 - i : i;
-        const int lo = s * nch / nseg * kT;
-        const int hi = min((s + 1) * nch / nseg * kT, len);
-        const float t = q[s * w];
-        q[s * w] = run;
-        run = fmaf(decay_pow(g2, max(hi - lo, 0)), run, t);
+    constexpr int kAhead = 8;
+    for (int i0 = 0; i0 < nseg; i0 += kAhead) {
+        float4 t[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i0 + i < nseg) t[i] = *reinterpret_cast<const float4*>(q + (rev ? nseg - 1 - i0 - i : i0 + i) * w);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (i0 + i >= nseg) break;
+            const int s = rev ? nseg - 1 - i0 - i : i0 + i;
+            *reinterpret_cast<float4*>(q + s * w) = run;
+            const float l = lam[s];
+            run = make_float4(fmaf(l, run.x, t[i].x), fmaf(l, run.y, t[i].y), fmaf(l, run.z, t[i].z), fmaf(l, run.w, t[i].w));
+        }
     }
-    if (last) last[bh * w + x] = run;
+    if (last) *reinterpret_cast<float4*>(last + bh * w + x) = run;
 }
 
 // [BH][L][cols] bf16 as a 3-D tensor, boxes of 64 columns x 128 tokens, 128-byte swizzle;
@@ -976,7 +1047,7 @@ cudaError_t launch1(const CUtensorMap& fs, const CUtensorMap& fq, const CUtensor
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = c.BH * p.nseg * (kMode == kOutF ? 1 : p.nfb);
-    kernel<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(fs, fq, es, eq, out, p);
+    kernel<<<static_cast<unsigned>(grid), threads(kMode), smem, st>>>(fs, fq, es, eq, out, p);
     return cudaGetLastError();
 }
 
@@ -1023,7 +1094,7 @@ cudaError_t segment_states(const DecayArgs& a, const Plan& c, const Carve& k, P&
     cudaError_t e = launch<kState>("tc_decay_state", fs, fs, es, es, fs, q, c, rev, a.norm, st);
     if (e != cudaSuccess) return e;
     TraceScope trace_("decay_seg_scan", st);
-    k_dec_seg_scan<<<dim3((a.F * 65 + 255) / 256, static_cast<unsigned>(c.BH)), 256, 0, st>>>(
+    k_dec_seg_scan<<<dim3((a.F * 65 + 1023) / 1024, static_cast<unsigned>(c.BH)), 256, 0, st>>>(
         k.st, a.norm ? k.sz : nullptr, first, first_z, last, last_z, a.F, c.nseg, rev, a.log_decay, a.lengths, a.H, a.L);
     p.first = k.st;
     p.first_z = k.sz;
