@@ -396,33 +396,29 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                         umma_commit(&bar[B_PF]);
                     }
                     wait_m(B_YF, i);
-                    for (int s = 0; s < ns; s += 2) {
+                    for (int s = 0; s < ns; s += 2) {   // while the scores are masked
                         slice(s);
                         if (s + 1 < ns) slice(s + 1);
+                        if (elect_one()) state_pair(s);
+                    }
+                    if (elect_one()) umma_commit(&bar[B_TF]);
+                    wait_m(B_PT, i);
+                    wait_m(B_MF, i);
+                    for (int r = 0; r < ns; ++r) {
+                        const int v = i * ns + r, ob = v & 1;
+                        if (v >= 2) wait_m(B_OE + ob, (v >> 1) - 1);
+                        const uint32_t oi = tmem + (ob ? kColOi : kColOi0), oe = tmem + (ob ? kColOe1 : kColOe0);
+                        const uint64_t du = d0 + oFs + ((i * nsE + r) & 3) * kTd;
                         if (elect_one()) {
-                            state_pair(s);
-                            if (s + 2 >= ns) umma_commit(&bar[B_TF]);
-                        }
-                        if (s == 0) {
-                            wait_m(B_PT, i);
-                            wait_m(B_MF, i);
-                        }
-                        for (int r = s; r < min(s + 2, ns); ++r) {
-                            const int v = i * ns + r, ob = v & 1;
-                            if (v >= 2) wait_m(B_OE + ob, (v >> 1) - 1);
-                            const uint32_t oi = tmem + (ob ? kColOi : kColOi0), oe = tmem + (ob ? kColOe1 : kColOe0);
-                            const uint64_t du = d0 + oFs + ((i * nsE + r) & 3) * kTd;
-                            if (elect_one()) {
 #pragma unroll
-                                for (int kk = 0; kk < 8; ++kk)
-                                    umma_bf16_ts(oi, tmem + kColP + 8 * kk, du + 128 * kk, idKM, kk > 0 ? 1u : 0u);
+                            for (int kk = 0; kk < 8; ++kk)
+                                umma_bf16_ts(oi, tmem + kColP + 8 * kk, du + 128 * kk, idKM, kk > 0 ? 1u : 0u);
 #pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    umma_bf16(oe, deq + 2 * kk, d0 + oM + r * kSd + 2 * kk, idKK, kk > 0 ? 1u : 0u);
-                                umma_commit(&bar[B_OF + ob]);
-                            }
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_bf16(oe, deq + 2 * kk, d0 + oM + r * kSd + 2 * kk, idKK, kk > 0 ? 1u : 0u);
+                            umma_commit(&bar[B_OF + ob]);
+                            if ((r & 1) || r == ns - 1) free_pair(r & ~1);
                         }
-                        if (elect_one()) free_pair(s);
                     }
                     if (elect_one()) {
                         umma_commit(&bar[B_OD]);
@@ -594,22 +590,23 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 tc_fence_before();
                 warp_arrive(&bar[B_OE + ob]);
                 const int fl = 64 * s + 32 * half;
-                if (has_z) {
-                    const float4* z4 = reinterpret_cast<const float4*>(zf + par * kMaxFw + fl);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float4 z = z4[c];
-                        e[4 * c] = __float_as_uint(fmaf(zc, z.x, __uint_as_float(e[4 * c])));
-                        e[4 * c + 1] = __float_as_uint(fmaf(zc, z.y, __uint_as_float(e[4 * c + 1])));
-                        e[4 * c + 2] = __float_as_uint(fmaf(zc, z.z, __uint_as_float(e[4 * c + 2])));
-                        e[4 * c + 3] = __float_as_uint(fmaf(zc, z.w, __uint_as_float(e[4 * c + 3])));
-                    }
-                }
                 uint32_t o[16];
+                const float2 fq2 = make_float2(fq, fq), zc2 = make_float2(zc, zc);
+                const float4* z4 = reinterpret_cast<const float4*>(zf + par * kMaxFw + fl);
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    o[c] = pack_bf16(fmaf(fq, __uint_as_float(e[2 * c]), __uint_as_float(a[2 * c])),
-                                     fmaf(fq, __uint_as_float(e[2 * c + 1]), __uint_as_float(a[2 * c + 1])));
+                for (int c = 0; c < 8; ++c) {
+                    float2 e0 = make_float2(__uint_as_float(e[4 * c]), __uint_as_float(e[4 * c + 1]));
+                    float2 e1 = make_float2(__uint_as_float(e[4 * c + 2]), __uint_as_float(e[4 * c + 3]));
+                    if (has_z) {
+                        const float4 z = z4[c];
+                        e0 = ffma2(zc2, make_float2(z.x, z.y), e0);
+                        e1 = ffma2(zc2, make_float2(z.z, z.w), e1);
+                    }
+                    e0 = ffma2(fq2, e0, make_float2(__uint_as_float(a[4 * c]), __uint_as_float(a[4 * c + 1])));
+                    e1 = ffma2(fq2, e1, make_float2(__uint_as_float(a[4 * c + 2]), __uint_as_float(a[4 * c + 3])));
+                    o[2 * c] = pack_bf16(e0.x, e0.y);
+                    o[2 * c + 1] = pack_bf16(e1.x, e1.y);
+                }
                 if (whole) {
                     if (lane == 0) bulk_wait_read<0>();   // the box's last store has read it
                     __syncwarp();
