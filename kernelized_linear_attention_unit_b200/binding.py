@@ -600,18 +600,32 @@ def slay_decode_step(q, k, v, S, z, out, R, m, seed, eps, stream=None):
 
 def _check_on(device, t, name, dtype=None, shape=None, optional=False):
     """_check, on `device`; None passes where the argument is optional."""
-    if t is None and optional:
-        return
+    if t is None:
+        if optional:
+            return
+    elif t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return   # as it should be (the device is a GPU: the first tensor went through _check)
     _check(t, name, dtype, shape)
     if t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
 
 
-def _stream_on(device, stream):
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if s.device != device:
-        raise ValueError("the stream is on %s, the tensors on %s" % (s.device, device))
-    return C.c_void_p(s.cuda_stream)
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call_on(device, stream, fn, name, args):
+    """fn(*args, stream) with `device` current; stream: the caller's, or that device's current one."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream.cuda_stream)
+    _raise(status, name)
 
 
 def _decay_pair(device, S, z, shape, normalize, name):
@@ -654,12 +668,11 @@ def slay_decay_attn_fwd(phq, phk, v, log_decay, out, den=None, normalize=True, e
     _decay_pair(dev, S_in, z_in, (B, H, F), normalize, "in")
     _decay_pair(dev, S_out, z_out, (B, H, F), normalize, "out")
     dt = _dt(phq)
-    with torch.cuda.device(dev):
-        workspace, wbytes = _decay_workspace(OP_DECAY_FWD, dt, B, H, L, F, Dv, workspace, dev)
-        _raise(lib().slay_decay_attn_fwd(
-            _ptr(phq), _ptr(phk), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(S_in), _ptr(z_in),
-            _ptr(out), _ptr(den), _ptr(S_out), _ptr(z_out), B, H, L, F, Dv, dt, int(bool(normalize)),
-            eps, _ptr(workspace), wbytes, _stream_on(dev, stream)), "slay_decay_attn_fwd")
+    workspace, wbytes = _decay_workspace(OP_DECAY_FWD, dt, B, H, L, F, Dv, workspace, dev)
+    _call_on(dev, stream, lib().slay_decay_attn_fwd, "slay_decay_attn_fwd", (
+        phq.data_ptr(), phk.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(lengths), _addr(S_in),
+        _addr(z_in), out.data_ptr(), _addr(den), _addr(S_out), _addr(z_out), B, H, L, F, Dv, dt,
+        1 if normalize else 0, eps, workspace.data_ptr(), wbytes))
     return workspace
 
 
@@ -680,13 +693,12 @@ def slay_decay_attn_bwd(phq, phk, v, log_decay, dout, dphq, dphk, dv, out=None, 
     _decay_pair(dev, dS_out, dz_out, (B, H, F), normalize, "out gradient")
     _decay_pair(dev, dS_in, dz_in, (B, H, F), normalize, "in gradient")
     dt = _dt(phq)
-    with torch.cuda.device(dev):
-        workspace, wbytes = _decay_workspace(OP_DECAY_BWD, dt, B, H, L, F, Dv, workspace, dev)
-        _raise(lib().slay_decay_attn_bwd(
-            _ptr(phq), _ptr(phk), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(S_in), _ptr(z_in),
-            _ptr(out), _ptr(den), _ptr(dout), _ptr(dS_out), _ptr(dz_out), _ptr(dphq), _ptr(dphk),
-            _ptr(dv), _ptr(dS_in), _ptr(dz_in), B, H, L, F, Dv, dt, int(bool(normalize)), eps,
-            _ptr(workspace), wbytes, _stream_on(dev, stream)), "slay_decay_attn_bwd")
+    workspace, wbytes = _decay_workspace(OP_DECAY_BWD, dt, B, H, L, F, Dv, workspace, dev)
+    _call_on(dev, stream, lib().slay_decay_attn_bwd, "slay_decay_attn_bwd", (
+        phq.data_ptr(), phk.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(lengths), _addr(S_in),
+        _addr(z_in), _addr(out), _addr(den), dout.data_ptr(), _addr(dS_out), _addr(dz_out),
+        dphq.data_ptr(), dphk.data_ptr(), dv.data_ptr(), _addr(dS_in), _addr(dz_in), B, H, L, F, Dv, dt,
+        1 if normalize else 0, eps, workspace.data_ptr(), wbytes))
     return workspace
 
 
@@ -708,11 +720,9 @@ def slay_decay_decode_step(phq, phk, v, log_decay, S, z, out, slots=None, normal
     _decay_pair(dev, S, z, (n, H, F), normalize, "pool")
     if slots is None and Bt > n:
         raise ValueError("%d rows, but the pool has %d slots" % (Bt, n))
-    with torch.cuda.device(dev):
-        _raise(lib().slay_decay_decode_step(
-            _ptr(phq), _ptr(phk), _ptr(v), _ptr(log_decay), _ptr(S), _ptr(z), _ptr(slots), _ptr(out),
-            Bt, H, F, Dv, n, _dt(phq), int(bool(normalize)), eps, _stream_on(dev, stream)),
-            "slay_decay_decode_step")
+    _call_on(dev, stream, lib().slay_decay_decode_step, "slay_decay_decode_step", (
+        phq.data_ptr(), phk.data_ptr(), v.data_ptr(), log_decay.data_ptr(), S.data_ptr(), _addr(z),
+        _addr(slots), out.data_ptr(), Bt, H, F, Dv, n, _dt(phq), 1 if normalize else 0, eps))
 
 
 def slay_state_copy(S_src, z_src, src, S_dst, z_dst, dst, stream=None):
@@ -730,7 +740,6 @@ def slay_state_copy(S_src, z_src, src, S_dst, z_dst, dst, stream=None):
     _check_on(dev, z_dst, "z_dst", torch.float32, (n_dst, H, F), optional=True)
     _check_on(dev, src, "src", torch.int32, (src.numel(),))
     _check_on(dev, dst, "dst", torch.int32, (src.numel(),))
-    with torch.cuda.device(dev):
-        _raise(lib().slay_state_copy(
-            _ptr(S_src), _ptr(z_src), _ptr(src), n_src, _ptr(S_dst), _ptr(z_dst), _ptr(dst), n_dst,
-            src.numel(), H, F, Dv, _stream_on(dev, stream)), "slay_state_copy")
+    _call_on(dev, stream, lib().slay_state_copy, "slay_state_copy", (
+        S_src.data_ptr(), _addr(z_src), src.data_ptr(), n_src, S_dst.data_ptr(), _addr(z_dst),
+        dst.data_ptr(), n_dst, src.numel(), H, F, Dv))
