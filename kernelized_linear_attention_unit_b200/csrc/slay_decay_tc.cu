@@ -59,8 +59,11 @@ __host__ __device__ constexpr int threads(int mode) { return 32 * (split(mode) ?
 // takes the other 64.  T of 128 features: the first limb's 64 columns, in the modes with
 // room a second limb's, and 16 for z.
 constexpr uint32_t kColP = 0, kColOi = 64, kColOe = 128, kColDen = 192;
-constexpr uint32_t kColOi0 = 128, kColOe0 = 192, kColOe1 = 256;   // kOutE: buffer 0; buffer 1 is kColOi, kColOe1
-__host__ __device__ constexpr uint32_t col_t(int mode) { return mode == kOutE ? 352 : 208; }
+// kOutE: two output buffers; the first limb's form puts the second one's Oi over the scores,
+// the two-limb form (128 features) has room beside them
+__host__ __device__ constexpr uint32_t col_oi(bool limbs, int b) { return limbs ? 128 + 128 * b : b ? 64 : 128; }
+__host__ __device__ constexpr uint32_t col_oe(bool limbs, int b) { return limbs ? 192 + 128 * b : b ? 256 : 192; }
+__host__ __device__ constexpr uint32_t col_t(int mode, bool limbs) { return limbs ? 384 : mode == kOutE ? 352 : 208; }
 __host__ __device__ constexpr uint32_t col_z(int mode) { return mode == kOutE ? 64 : 128; }
 __host__ __device__ constexpr uint32_t t_stride(int mode) { return mode == kOutE ? 80 : 144; }
 __host__ __device__ constexpr int limb_tiles(int mode) { return mode == kState ? 6 : mode == kOutE ? 2 : 3; }
@@ -176,6 +179,10 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     constexpr bool kSplit = split(kMode);
     constexpr int kThreads = threads(kMode), kEs = kMode == kOutF ? 1 : 2;
     constexpr bool kCols = kRev && kNorm, kRows = kMode == kOutE && !kRev && kNorm, kDen = kMode == kOutF && !kRev && kNorm;
+    // The normalized dphq is a difference (c_ij has no weighted mean over j) that loses a bit or
+    // two: its scores and its copy of the state go in as two bf16 limbs, over half as many
+    // features a CTA (one limb: 3.1e-3 off in relative L2, two: 1.7e-3, bf16's own rounding).
+    constexpr bool kLimb = kRows;
     constexpr Layout Lo = layout(kMode);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Lo.bar);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Lo.tmem);
@@ -312,7 +319,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 };
                 auto state_pair = [&](int s) {   // T of the pair of slices s, s + 1
                     const uint64_t da = dT + oFs + ((i * nsE + s) & 3) * kTd;
-                    const uint32_t t = tmem + col_t(kMode) + t_stride(kMode) * (s >> 1);
+                    const uint32_t t = tmem + col_t(kMode, kLimb) + t_stride(kMode) * (s >> 1);
                     const uint32_t oy = oY + (kMode == kState ? eb * 3 * kTd : 0);
                     int l = 0;
                     if (kMode != kOutE && nl > 1) {   // two limbs side by side: the F side is read once
@@ -388,7 +395,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                     wait_m(B_ESF + eb, i / kEs);
                     if (clear) clear_rows(Lo.es + eb * kTile);
                     const int v1 = i * ns - 1, vo = (v1 & 1) ? v1 : v1 - 1;   // last use of the buffer over P
-                    if (vo >= 1) wait_m(B_OE + 1, vo >> 1);
+                    if (!kLimb && vo >= 1) wait_m(B_OE + 1, vo >> 1);
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -407,15 +414,23 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                     for (int r = 0; r < ns; ++r) {
                         const int v = i * ns + r, ob = v & 1;
                         if (v >= 2) wait_m(B_OE + ob, (v >> 1) - 1);
-                        const uint32_t oi = tmem + (ob ? kColOi : kColOi0), oe = tmem + (ob ? kColOe1 : kColOe0);
+                        const uint32_t oi = tmem + col_oi(kLimb, ob), oe = tmem + col_oe(kLimb, ob);
                         const uint64_t du = d0 + oFs + ((i * nsE + r) & 3) * kTd;
                         if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
                                 umma_bf16_ts(oi, tmem + kColP + 8 * kk, du + 128 * kk, idKM, kk > 0 ? 1u : 0u);
+                            if (kLimb)
+#pragma unroll
+                                for (int kk = 0; kk < 8; ++kk)
+                                    umma_bf16_ts(oi, tmem + kColP + 64 + 8 * kk, du + 128 * kk, idKM, 1u);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 umma_bf16(oe, deq + 2 * kk, d0 + oM + r * kSd + 2 * kk, idKK, kk > 0 ? 1u : 0u);
+                            if (kLimb)
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    umma_bf16(oe, deq + 2 * kk, d0 + oM + (r + 2) * kSd + 2 * kk, idKK, 1u);
                             umma_commit(&bar[B_OF + ob]);
                             if ((r & 1) || r == ns - 1) free_pair(r & ~1);
                         }
@@ -481,14 +496,19 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
             wait_k(B_PF, i);
             tc_fence_after();
             float2 rs = make_float2(0.0f, 0.0f);
-            uint32_t pk[2][16];
+            uint32_t pk[2][16], pl[2][16];   // P~ in one limb or two
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
                 const int cb = half + 2 * hh, j0 = 32 * cb;
                 const int side = kRev ? cb - q : q - cb;   // > 0: inside, 0: diagonal
+                auto put = [&](int c, float2 x) {
+                    const uint32_t l = pack_bf16(x.x, x.y);
+                    pk[hh][c / 2] = l;
+                    if (kLimb) pl[hh][c / 2] = pack_bf16(x.x - bf_lo(l), x.y - bf_hi(l));
+                };
                 if (side < 0) {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) pk[hh][c] = 0u;
+                    for (int c = 0; c < 16; ++c) pk[hh][c] = pl[hh][c] = 0u;
                     continue;
                 }
                 uint32_t r[32];
@@ -512,10 +532,8 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                             rs = ffma2(s0, w0, rs);
                             rs = ffma2(s1, w1, rs);
                         }
-                        s0 = fmul2(s0, w0);
-                        s1 = fmul2(s1, w1);
-                        pk[hh][c / 2] = pack_bf16(s0.x, s0.y);
-                        pk[hh][c / 2 + 1] = pack_bf16(s1.x, s1.y);
+                        put(c, fmul2(s0, w0));
+                        put(c + 2, fmul2(s1, w1));
                     }
                 } else {
                     const float* pd = pw + 31 + (kRev ? -lane : lane);
@@ -542,18 +560,21 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                             rs.x += s0.x + s1.x;
                             rs.y += s0.y + s1.y;
                         }
-                        pk[hh][c / 2] = pack_bf16(s0.x, s0.y);
-                        pk[hh][c / 2 + 1] = pack_bf16(s1.x, s1.y);
+                        put(c, s0);
+                        put(c + 2, s1);
                     }
                 }
             }
-            if (kMode == kOutF && kDen) dsum[(par * 2 + half) * kT + row] = rs.x + rs.y;
+            if (kDen) dsum[(par * 2 + half) * kT + row] = rs.x + rs.y;
             // P~ goes over the scores once both warps of these rows have read theirs
             tc_fence_before();
             named_bar_sync(1 + q, 64);
             tc_fence_after();
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) tmem_st16(trow + kColP + 16 * (half + 2 * hh), pk[hh]);
+            for (int hh = 0; hh < 2; ++hh) {
+                tmem_st16(trow + kColP + 16 * (half + 2 * hh), pk[hh]);
+                if (kLimb) tmem_st16(trow + kColP + 64 + 16 * (half + 2 * hh), pl[hh]);
+            }
             tmem_wait_st();
             // (before PT: no barrier may run two phases ahead of a thread that waits on it)
             if (kMode == kOutE && has_z) wait_k(B_MF, i);   // zf of this chunk
@@ -582,8 +603,8 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 wait_k(B_OF + ob, v >> 1);
                 tc_fence_after();
                 uint32_t a[32], e[32];
-                tmem_ld32(trow + (ob ? kColOi : kColOi0) + 32 * half, a);
-                tmem_ld32(trow + (ob ? kColOe1 : kColOe0) + 32 * half, e);
+                tmem_ld32(trow + col_oi(kLimb, ob) + 32 * half, a);
+                tmem_ld32(trow + col_oe(kLimb, ob) + 32 * half, e);
                 tmem_wait_ld();
                 reg_fence(a);
                 reg_fence(e);
@@ -666,6 +687,18 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                         st_shared_v4(slab + sw128_off(f & 63, 4 * half + c),
                                      pack_bf16(run[b][8 * c], run[b][8 * c + 1]), pack_bf16(run[b][8 * c + 2], run[b][8 * c + 3]),
                                      pack_bf16(run[b][8 * c + 4], run[b][8 * c + 5]), pack_bf16(run[b][8 * c + 6], run[b][8 * c + 7]));
+                    if (kLimb && b == 0)   // the second limb, two slabs on
+#pragma unroll
+                        for (int c = 0; c < kW / 8; ++c) {
+                            uint32_t l[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float x = run[b][8 * c + 2 * k], y = run[b][8 * c + 2 * k + 1];
+                                const uint32_t hi = pack_bf16(x, y);
+                                l[k] = pack_bf16(x - bf_lo(hi), y - bf_hi(hi));
+                            }
+                            st_shared_v4(slab + 2 * kSlab + sw128_off(f & 63, 4 * half + c), l[0], l[1], l[2], l[3]);
+                        }
                     if (has_zrow(b)) {
                         if (kMode == kOutF) {
                             uint16_t l[3];
@@ -757,7 +790,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                     wait_k(B_TF + b, i);
                     tc_fence_after();
                 }
-                const uint32_t tc = trow + col_t(kMode) + t_stride(kMode) * b;
+                const uint32_t tc = trow + col_t(kMode, kLimb) + t_stride(kMode) * b;
 #pragma unroll
                 for (int hh = 0; hh < kW / 32; ++hh) {
                 uint32_t t[32], t2[32], z0 = 0, z1 = 0, z2 = 0;
@@ -983,21 +1016,35 @@ bool map_rows(CUtensorMap* m, const void* base, int cols, int L, int64_t BH, boo
               out ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a call is cut: feature blocks of at most 256, and segments of the sequence.
+// How a sweep is cut: blocks of at most `most` features, and segments of the sequence so that
+// the CTAs fill the GPU (one a SM).
 struct Plan {
     int nfb, fw, nseg;
     int64_t BH;
 };
 
-Plan plan(const DecayArgs& a)
+Plan plan(const DecayArgs& a, int most, bool blocks_in_grid)
 {
     Plan c{};
     c.BH = static_cast<int64_t>(a.B) * a.H;
-    c.nfb = (a.F + kMaxFw - 1) / kMaxFw;
+    c.nfb = (a.F + most - 1) / most;
     c.fw = ((a.F + c.nfb - 1) / c.nfb + 63) & ~63;
+    const int64_t units = c.BH * (blocks_in_grid ? c.nfb : 1);
     const int nch = (a.L + kT - 1) / kT;
-    c.nseg = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kNumSMs / c.BH, nch)));
+    c.nseg = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kNumSMs / units, nch)));
     return c;
+}
+
+// out, dv, dphk: the feature blocks of a 64-wide output follow one another, so (b, h) and
+// segments fill the GPU; dphk shares dv's segments and their states.
+Plan plan_f(const DecayArgs& a) { return plan(a, kMaxFw, false); }
+// dphq: the normalized form's two limbs leave room for 128 features; otherwise 256, unless
+// blocks of 128 fill the GPU without segments, whose states are a pass of their own.
+Plan plan_q(const DecayArgs& a)
+{
+    const Plan h = plan(a, kMaxFw / 2, true);
+    if (a.norm || (h.nseg == 1 && h.BH * h.nfb <= kNumSMs)) return h;
+    return plan(a, kMaxFw, true);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1007,7 +1054,7 @@ struct Carve {
     size_t bytes;
 };
 
-Carve carve(const DecayArgs& a, const Plan& c, bool bwd, void* ws)
+Carve carve(const DecayArgs& a, bool bwd, void* ws)
 {
     char* base = static_cast<char*>(ws);
     size_t o = 0;
@@ -1017,10 +1064,12 @@ Carve carve(const DecayArgs& a, const Plan& c, bool bwd, void* ws)
         return q;
     };
     Carve k{};
+    const Plan c = plan_f(a);
     const size_t rows = static_cast<size_t>(c.BH) * a.L;
-    if (c.nseg > 1) {
-        k.st = take(static_cast<size_t>(c.BH) * c.nseg * a.F * 64);
-        k.sz = take(static_cast<size_t>(c.BH) * c.nseg * a.F);
+    const int nseg = bwd ? std::max(c.nseg, plan_q(a).nseg) : c.nseg;
+    if (nseg > 1) {
+        k.st = take(static_cast<size_t>(c.BH) * nseg * a.F * 64);
+        k.sz = take(static_cast<size_t>(c.BH) * nseg * a.F);
     }
     if (c.nfb > 1) {
         k.part = take(rows * 64);
@@ -1084,11 +1133,18 @@ cudaError_t segment_states(const DecayArgs& a, const Plan& c, const Carve& k, P&
     p.first = first;
     p.first_z = first_z;
     if (c.nseg == 1) return cudaSuccess;
+    const Plan cs = [&] {   // (the sums themselves go by blocks of 256 whatever the sweep's)
+        Plan x = plan(a, kMaxFw, true);
+        x.nseg = c.nseg;
+        return x;
+    }();
     P q = p;
+    q.nfb = cs.nfb;
+    q.fw = cs.fw;
     q.first = q.first_z = nullptr;
     q.last = k.st;
     q.last_z = k.sz;
-    cudaError_t e = launch<kState>("tc_decay_state", fs, fs, es, es, fs, q, c, rev, a.norm, st);
+    cudaError_t e = launch<kState>("tc_decay_state", fs, fs, es, es, fs, q, cs, rev, a.norm, st);
     if (e != cudaSuccess) return e;
     TraceScope trace_("decay_seg_scan", st);
     k_dec_seg_scan<<<dim3((a.F * 65 + 1023) / 1024, static_cast<unsigned>(c.BH)), 256, 0, st>>>(
@@ -1121,12 +1177,12 @@ bool decay_tc_supported(const DecayArgs& a)
     return a.dt == SLAY_BF16 && a.L > 0 && a.F % 8 == 0 && a.F <= 2 * kMaxFw;
 }
 
-size_t decay_tc_ws(const DecayArgs& a, bool bwd) { return carve(a, plan(a), bwd, nullptr).bytes; }
+size_t decay_tc_ws(const DecayArgs& a, bool bwd) { return carve(a, bwd, nullptr).bytes; }
 
 cudaError_t decay_tc_fwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st)
 {
-    const Plan c = plan(a);
-    const Carve k = carve(a, c, false, ws);
+    const Plan c = plan_f(a);
+    const Carve k = carve(a, false, ws);
     CUtensorMap mq, mk, mv;
     if (!map_rows(&mq, a.phq, a.F, a.L, c.BH) || !map_rows(&mk, a.phk, a.F, a.L, c.BH) || !map_rows(&mv, a.v, 64, a.L, c.BH))
         return cudaErrorInvalidValue;
@@ -1144,8 +1200,8 @@ cudaError_t decay_tc_fwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
 
 cudaError_t decay_tc_bwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st)
 {
-    const Plan c = plan(a);
-    const Carve k = carve(a, c, true, ws);
+    const Plan c = plan_f(a), cq = plan_q(a);
+    const Carve k = carve(a, true, ws);
     CUtensorMap mq, mk, mv, mo, mdq, mdk;
     if (!map_rows(&mq, a.phq, a.F, a.L, c.BH) || !map_rows(&mk, a.phk, a.F, a.L, c.BH) ||
         !map_rows(&mv, a.v, 64, a.L, c.BH) || !map_rows(&mo, a.dout, 64, a.L, c.BH) ||
@@ -1154,12 +1210,12 @@ cudaError_t decay_tc_bwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
     cudaError_t e = a.norm ? decay_row_stats(a, k.rz, k.r, st) : cudaSuccess;
     if (e != cudaSuccess) return e;
     const float *rz = a.norm ? k.rz : nullptr, *r = a.norm ? k.r : nullptr;
-    P s = base(a, c, err);   // dphq from the states before each token
-    if ((e = segment_states(a, c, k, s, mk, mv, false, a.S_in, a.z_in, nullptr, nullptr, st)) != cudaSuccess) return e;
+    P s = base(a, cq, err);   // dphq from the states before each token
+    if ((e = segment_states(a, cq, k, s, mk, mv, false, a.S_in, a.z_in, nullptr, nullptr, st)) != cudaSuccess) return e;
     s.q_mul = rz;
     s.q_off = r;
     s.o = static_cast<__nv_bfloat16*>(a.dphq);
-    if ((e = launch<kOutE>("tc_decay_out_e", mk, mk, mv, mo, mdq, s, c, false, a.norm, st)) != cudaSuccess) return e;
+    if ((e = launch<kOutE>("tc_decay_out_e", mk, mk, mv, mo, mdq, s, cq, false, a.norm, st)) != cudaSuccess) return e;
     P g = base(a, c, err);   // dphk and dv from the states after each token
     g.s_mul = rz;
     g.s_off = r;
