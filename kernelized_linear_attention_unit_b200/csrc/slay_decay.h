@@ -38,6 +38,32 @@ __device__ __forceinline__ float decay_pow(float log2_lam, int k)
     return k == 0 ? 1.0f : exp2f(static_cast<float>(k) * log2_lam);
 }
 
+// The kernels of one call follow one another on the call's stream.  Each but the first is
+// launched while the one before it still runs (programmatic stream serialization): its blocks
+// set themselves up and then wait here until everything before them is complete and visible.
+__device__ __forceinline__ void after_previous_kernel()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_in_chain(bool first, void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                            Args... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = first ? 0 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Arguments of the decayed forward and backward, as the entry points take them.
@@ -62,6 +88,7 @@ struct DecayArgs {
 };
 
 // Row statistics of the normalized backward: rz = 1 / (den + eps), r = out . dout, [B,H,L].
+// (the first kernel of its call)
 cudaError_t decay_row_stats(const DecayArgs& a, float* rz, float* r, cudaStream_t st);
 
 // CUDA cores: any F up to kMaxF, fp32 or bf16 operands, fp32 arithmetic.

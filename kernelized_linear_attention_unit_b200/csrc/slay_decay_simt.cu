@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kNT) k_dec_state(Sweep s)
     const float g2 = s.log_decay[bh % s.H] * kLog2e;
     float* st = s.st + ((bh * s.nc + c) * s.F + f0) * 64;
     const int64_t row0 = bh * s.L + t0;
+    after_previous_kernel();
     if (tid < kC) {
         float a = 0.0f, b = 0.0f;
         if (tid < n) {
@@ -213,36 +214,50 @@ __global__ void __launch_bounds__(kNT) k_dec_state(Sweep s)
     }
 }
 
-// Chunk states -> the state entering each chunk (in place); first: the state entering the
-// walk (null: zero), last: the one leaving it (null: not wanted; may be `first` itself, each
-// element is read before it is written).  grid (ceil(nelem / kNT), BH), W = 64 (S) or 1 (z).
-__global__ void __launch_bounds__(kNT) k_dec_scan(float* st, const float* first, float* last, int64_t nelem,
-                                                  int nc, bool rev, const float* log_decay,
-                                                  const int32_t* lengths, int H, int L)
+// Chunk states -> the state entering each chunk (in place), S and z in one launch; first: the
+// state entering the walk (null: zero), last: the one leaving it (null: not wanted; may be
+// `first` itself, each element is read before it is written).  Loads run eight chunks ahead.
+// grid (ceil(64 F / 4 kNT) + ceil(F / kNT), BH): a thread has four elements of S or one of z
+// (whose rows need not be whole float4s).
+__global__ void __launch_bounds__(kNT) k_dec_scan(Sweep s, const float* first, const float* first_z, float* last,
+                                                  float* last_z, int s_blocks)
 {
-    const int64_t bh = blockIdx.y, x = static_cast<int64_t>(blockIdx.x) * kNT + threadIdx.x;
-    if (x >= nelem) return;
-    const int n = seq_len(lengths, static_cast<int>(bh / H), L);
-    const float g2 = log_decay[bh % H] * kLog2e;
+    after_previous_kernel();
+    const int64_t bh = blockIdx.y;
+    const int n = seq_len(s.lengths, static_cast<int>(bh / s.H), s.L);
+    const float g2 = s.log_decay[bh % s.H] * kLog2e;
     const float lam_c = decay_pow(g2, kC);
-    float run = first ? first[bh * nelem + x] : 0.0f;
-    float* p = st + bh * nc * nelem + x;
     constexpr int kAhead = 8;
-    for (int i0 = 0; i0 < nc; i0 += kAhead) {
-        float t[kAhead];
+    auto walk = [&](auto* p, const auto* from, auto* to, int64_t w, int64_t x, auto zero, auto step) {
+        auto run = from ? from[bh * w + x] : zero;
+        p += bh * s.nc * w + x;
+        for (int i0 = 0; i0 < s.nc; i0 += kAhead) {
+            decltype(run) t[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (i0 + i < nc) t[i] = p[(rev ? nc - 1 - i0 - i : i0 + i) * nelem];
+            for (int i = 0; i < kAhead; ++i)
+                if (i0 + i < s.nc) t[i] = p[(s.rev ? s.nc - 1 - i0 - i : i0 + i) * w];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (i0 + i < nc) {
-                const int c = rev ? nc - 1 - i0 - i : i0 + i;
-                p[c * nelem] = run;
+            for (int i = 0; i < kAhead; ++i) {
+                if (i0 + i >= s.nc) break;
+                const int c = s.rev ? s.nc - 1 - i0 - i : i0 + i;
+                p[c * w] = run;
                 const int nn = min(max(n - c * kC, 0), kC);
-                run = fmaf(nn == kC ? lam_c : decay_pow(g2, nn), run, t[i]);
+                run = step(nn == kC ? lam_c : decay_pow(g2, nn), run, t[i]);
             }
+        }
+        if (to) to[bh * w + x] = run;
+    };
+    if (static_cast<int>(blockIdx.x) < s_blocks) {
+        const int64_t x = static_cast<int64_t>(blockIdx.x) * kNT + threadIdx.x, w = static_cast<int64_t>(s.F) * 16;
+        if (x < w)
+            walk(reinterpret_cast<float4*>(s.st), reinterpret_cast<const float4*>(first), reinterpret_cast<float4*>(last), w, x,
+                 make_float4(0.f, 0.f, 0.f, 0.f), [](float l, float4 a, float4 b) {
+                     return make_float4(fmaf(l, a.x, b.x), fmaf(l, a.y, b.y), fmaf(l, a.z, b.z), fmaf(l, a.w, b.w));
+                 });
+    } else {
+        const int64_t x = static_cast<int64_t>(blockIdx.x - s_blocks) * kNT + threadIdx.x;
+        if (x < s.F) walk(s.sz, first_z, last_z, s.F, x, 0.0f, [](float l, float a, float b) { return fmaf(l, a, b); });
     }
-    if (last) last[bh * nelem + x] = run;
 }
 
 // Masked, decayed scores: query row i, state token j of a chunk of n.
@@ -267,6 +282,7 @@ __global__ void __launch_bounds__(kNT) k_dec_out_f(Sweep s, T* o, float* den, bo
     const int64_t bh = blockIdx.y;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int t0 = c * kC, n = min(kC, seq_len(s.lengths, static_cast<int>(bh / s.H), s.L) - t0);
+    after_previous_kernel();
     if (n <= 0) return;
     const float g2 = s.log_decay[bh % s.H] * kLog2e;
     const int64_t row0 = bh * s.L + t0;
@@ -354,6 +370,7 @@ __global__ void __launch_bounds__(kNT) k_dec_out_e(Sweep s, T* o, bool norm)
     const int64_t bh = blockIdx.y;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int t0 = c * kC, n = min(kC, seq_len(s.lengths, static_cast<int>(bh / s.H), s.L) - t0);
+    after_previous_kernel();
     if (n <= 0) return;
     const float g2 = s.log_decay[bh % s.H] * kLog2e;
     const int64_t row0 = bh * s.L + t0;
@@ -456,20 +473,21 @@ constexpr size_t kSmemF = 3 * 64 * kPitch * sizeof(float), kSmemE = 4 * 64 * kPi
 
 template <typename T>
 cudaError_t states(const Sweep& s, int64_t BH, const float* first, const float* first_z, float* last, float* last_z,
-                   cudaStream_t st)
+                   bool& chained, cudaStream_t st)
 {
+    cudaError_t e = cudaSuccess;
     if (s.nc > 0) {   // L == 0: the walk has no chunk and hands its state on
         TraceScope trace_("simt_decay_state", st);
-        k_dec_state<T><<<dim3(s.nc, (s.F + 63) / 64, static_cast<unsigned>(BH)), kNT, kSmemS, st>>>(s);
+        e = launch_in_chain(!chained, k_dec_state<T>, dim3(s.nc, (s.F + 63) / 64, static_cast<unsigned>(BH)), kNT, kSmemS, st, s);
+        chained = true;
+        if (e != cudaSuccess) return e;
     }
-    const int64_t ne = static_cast<int64_t>(s.F) * 64;
+    const int sb = (s.F * 16 + kNT - 1) / kNT, zb = s.sz ? (s.F + kNT - 1) / kNT : 0;
     TraceScope trace_("simt_decay_scan", st);
-    k_dec_scan<<<dim3(static_cast<unsigned>((ne + kNT - 1) / kNT), static_cast<unsigned>(BH)), kNT, 0, st>>>(
-        s.st, first, last, ne, s.nc, s.rev, s.log_decay, s.lengths, s.H, s.L);
-    if (s.sz)
-        k_dec_scan<<<dim3((s.F + kNT - 1) / kNT, static_cast<unsigned>(BH)), kNT, 0, st>>>(
-            s.sz, first_z, last_z, s.F, s.nc, s.rev, s.log_decay, s.lengths, s.H, s.L);
-    return cudaGetLastError();
+    e = launch_in_chain(!chained, k_dec_scan, dim3(sb + zb, static_cast<unsigned>(BH)), kNT, 0, st, s, first, first_z, last,
+                        last_z, sb);
+    chained = true;
+    return e;
 }
 
 template <typename T>
@@ -528,15 +546,15 @@ cudaError_t fwd_t(const DecayArgs& a, void* ws, cudaStream_t st)
     const int64_t BH = static_cast<int64_t>(a.B) * a.H;
     cudaError_t e = prepare_smem<T>();
     if (e != cudaSuccess) return e;
+    bool chained = false;   // whether a kernel of this call runs before
     Sweep s = base(a, c);
     s.fq = a.phq;
     s.fs = a.phk;
     s.es = a.v;
-    if ((e = states<T>(s, BH, a.S_in, a.z_in, a.S_out, a.z_out, st)) != cudaSuccess || s.nc == 0) return e;
+    if ((e = states<T>(s, BH, a.S_in, a.z_in, a.S_out, a.z_out, chained, st)) != cudaSuccess || s.nc == 0) return e;
     TraceScope trace_("simt_decay_out", st);
-    k_dec_out_f<T><<<dim3(s.nc, static_cast<unsigned>(BH)), kNT, kSmemF, st>>>(s, static_cast<T*>(a.out_w), a.den_w, a.norm,
-                                                                             a.eps);
-    return cudaGetLastError();
+    return launch_in_chain(false, k_dec_out_f<T>, dim3(s.nc, static_cast<unsigned>(BH)), kNT, kSmemF, st, s,
+                           static_cast<T*>(a.out_w), a.den_w, a.norm, a.eps);
 }
 
 template <typename T>
@@ -547,6 +565,7 @@ cudaError_t bwd_t(const DecayArgs& a, void* ws, cudaStream_t st)
     cudaError_t e = prepare_smem<T>();
     if (e != cudaSuccess) return e;
     if (a.norm && a.L > 0 && (e = decay_row_stats(a, c.rz, c.r, st)) != cudaSuccess) return e;
+    bool chained = a.norm && a.L > 0;   // whether a kernel of this call runs before
     const float *rz = a.norm ? c.rz : nullptr, *r = a.norm ? c.r : nullptr;
     // few CTAs: the column blocks of the F-wide outputs go to CTAs of their own
     const int nfb = (a.F + 63) / 64, nc = (a.L + kC - 1) / kC;
@@ -558,9 +577,11 @@ cudaError_t bwd_t(const DecayArgs& a, void* ws, cudaStream_t st)
     s.q_mul = rz;
     s.q_off = r;
     if (nc > 0) {
-        if ((e = states<T>(s, BH, a.S_in, a.z_in, nullptr, nullptr, st)) != cudaSuccess) return e;
+        if ((e = states<T>(s, BH, a.S_in, a.z_in, nullptr, nullptr, chained, st)) != cudaSuccess) return e;
         TraceScope trace_("simt_decay_out", st);
-        k_dec_out_e<T><<<dim3(nc, static_cast<unsigned>(BH), zsplit), kNT, kSmemE, st>>>(s, static_cast<T*>(a.dphq), a.norm);
+        e = launch_in_chain(false, k_dec_out_e<T>, dim3(nc, static_cast<unsigned>(BH), zsplit), kNT, kSmemE, st, s,
+                            static_cast<T*>(a.dphq), a.norm);
+        if (e != cudaSuccess) return e;
     }
     Sweep g = base(a, c);   // dphk and dv from the backward states
     g.rev = true;
@@ -571,11 +592,13 @@ cudaError_t bwd_t(const DecayArgs& a, void* ws, cudaStream_t st)
     g.z_delta = a.norm;
     g.eq = a.v;
     g.fq = a.phk;
-    if ((e = states<T>(g, BH, a.dS_out, a.dz_out, a.dS_in, a.dz_in, st)) != cudaSuccess || nc == 0) return e;
+    if ((e = states<T>(g, BH, a.dS_out, a.dz_out, a.dS_in, a.dz_in, chained, st)) != cudaSuccess || nc == 0) return e;
     TraceScope trace_("simt_decay_out", st);
-    k_dec_out_e<T><<<dim3(nc, static_cast<unsigned>(BH), zsplit), kNT, kSmemE, st>>>(g, static_cast<T*>(a.dphk), a.norm);
-    k_dec_out_f<T><<<dim3(nc, static_cast<unsigned>(BH)), kNT, kSmemF, st>>>(g, static_cast<T*>(a.dv), nullptr, false, 0.0f);
-    return cudaGetLastError();
+    e = launch_in_chain(false, k_dec_out_e<T>, dim3(nc, static_cast<unsigned>(BH), zsplit), kNT, kSmemE, st, g,
+                        static_cast<T*>(a.dphk), a.norm);
+    if (e != cudaSuccess) return e;
+    return launch_in_chain(false, k_dec_out_f<T>, dim3(nc, static_cast<unsigned>(BH)), kNT, kSmemF, st, g, static_cast<T*>(a.dv),
+                           nullptr, false, 0.0f);
 }
 
 }  // namespace

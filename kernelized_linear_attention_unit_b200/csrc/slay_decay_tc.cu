@@ -232,6 +232,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    after_previous_kernel();
     constexpr uint32_t tmem = 0;   // all 512 columns are this CTA's
     Bounded wt;
     if (*tslot != tmem) {
@@ -969,6 +970,7 @@ __global__ void __launch_bounds__(256) k_dec_seg_scan(float* st, float* sz, cons
         for (int s = threadIdx.x; s < nseg; s += 256)
             lam[s] = decay_pow(g2, max(min((s + 1) * nch / nseg * kT, len) - s * nch / nseg * kT, 0));
     }
+    after_previous_kernel();
     __syncthreads();
     int x = (blockIdx.x * 256 + threadIdx.x) * 4;
     int64_t w = static_cast<int64_t>(F) * 64;
@@ -1085,7 +1087,7 @@ Carve carve(const DecayArgs& a, bool bwd, void* ws)
 
 template <int kMode, bool kRev, bool kNorm>
 cudaError_t launch1(const CUtensorMap& fs, const CUtensorMap& fq, const CUtensorMap& es, const CUtensorMap& eq,
-                    const CUtensorMap& out, const P& p, const Plan& c, cudaStream_t st)
+                    const CUtensorMap& out, const P& p, const Plan& c, bool& chained, cudaStream_t st)
 {
     constexpr size_t smem = layout(kMode).total + 1024;
     static_assert(smem <= 232448, "shared memory of one CTA");
@@ -1093,18 +1095,19 @@ cudaError_t launch1(const CUtensorMap& fs, const CUtensorMap& fq, const CUtensor
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = c.BH * p.nseg * (kMode == kOutF ? 1 : p.nfb);
-    kernel<<<static_cast<unsigned>(grid), threads(kMode), smem, st>>>(fs, fq, es, eq, out, p);
-    return cudaGetLastError();
+    const bool first = !chained;
+    chained = true;
+    return launch_in_chain(first, +kernel, dim3(static_cast<unsigned>(grid)), threads(kMode), smem, st, fs, fq, es, eq, out, p);
 }
 
 template <int kMode>
 cudaError_t launch(const char* name, const CUtensorMap& fs, const CUtensorMap& fq, const CUtensorMap& es,
                    const CUtensorMap& eq, const CUtensorMap& out, const P& p, const Plan& c, bool rev, bool norm,
-                   cudaStream_t st)
+                   bool& chained, cudaStream_t st)
 {
     TraceScope trace_(name, st);
-    if (rev) return norm ? launch1<kMode, true, true>(fs, fq, es, eq, out, p, c, st) : launch1<kMode, true, false>(fs, fq, es, eq, out, p, c, st);
-    return norm ? launch1<kMode, false, true>(fs, fq, es, eq, out, p, c, st) : launch1<kMode, false, false>(fs, fq, es, eq, out, p, c, st);
+    if (rev) return norm ? launch1<kMode, true, true>(fs, fq, es, eq, out, p, c, chained, st) : launch1<kMode, true, false>(fs, fq, es, eq, out, p, c, chained, st);
+    return norm ? launch1<kMode, false, true>(fs, fq, es, eq, out, p, c, chained, st) : launch1<kMode, false, false>(fs, fq, es, eq, out, p, c, chained, st);
 }
 
 P base(const DecayArgs& a, const Plan& c, int* err)
@@ -1128,7 +1131,7 @@ P base(const DecayArgs& a, const Plan& c, int* err)
 // is left for when there is one segment).
 cudaError_t segment_states(const DecayArgs& a, const Plan& c, const Carve& k, P& p, const CUtensorMap& fs,
                            const CUtensorMap& es, bool rev, const float* first, const float* first_z, float* last,
-                           float* last_z, cudaStream_t st)
+                           float* last_z, bool& chained, cudaStream_t st)
 {
     p.first = first;
     p.first_z = first_z;
@@ -1144,27 +1147,27 @@ cudaError_t segment_states(const DecayArgs& a, const Plan& c, const Carve& k, P&
     q.first = q.first_z = nullptr;
     q.last = k.st;
     q.last_z = k.sz;
-    cudaError_t e = launch<kState>("tc_decay_state", fs, fs, es, es, fs, q, cs, rev, a.norm, st);
+    cudaError_t e = launch<kState>("tc_decay_state", fs, fs, es, es, fs, q, cs, rev, a.norm, chained, st);
     if (e != cudaSuccess) return e;
     TraceScope trace_("decay_seg_scan", st);
-    k_dec_seg_scan<<<dim3((a.F * 65 + 1023) / 1024, static_cast<unsigned>(c.BH)), 256, 0, st>>>(
-        k.st, a.norm ? k.sz : nullptr, first, first_z, last, last_z, a.F, c.nseg, rev, a.log_decay, a.lengths, a.H, a.L);
+    e = launch_in_chain(false, k_dec_seg_scan, dim3((a.F * 65 + 1023) / 1024, static_cast<unsigned>(c.BH)), 256, 0, st, k.st,
+                        a.norm ? k.sz : nullptr, first, first_z, last, last_z, a.F, c.nseg, rev, a.log_decay, a.lengths, a.H, a.L);
     p.first = k.st;
     p.first_z = k.sz;
-    return cudaGetLastError();
+    return e;
 }
 
 // A sweep whose queries are on the F side: one launch per feature block, the blocks'
 // numerators and denominators added in fp32.
 cudaError_t out_f(const CUtensorMap& fs, const CUtensorMap& fq, const CUtensorMap& es, P p, const Plan& c,
-                  const Carve& k, bool rev, bool norm, cudaStream_t st)
+                  const Carve& k, bool rev, bool norm, bool& chained, cudaStream_t st)
 {
     p.part = k.part;
     p.part_den = k.part_den;
     for (int fb = 0; fb < c.nfb; ++fb) {
         p.fb0 = fb;
         p.part_mode = c.nfb == 1 ? 0 : fb == 0 ? 1 : 2;
-        const cudaError_t e = launch<kOutF>("tc_decay_out_f", fs, fq, es, es, fs, p, c, rev, norm, st);
+        const cudaError_t e = launch<kOutF>("tc_decay_out_f", fs, fq, es, es, fs, p, c, rev, norm, chained, st);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -1187,7 +1190,8 @@ cudaError_t decay_tc_fwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
     if (!map_rows(&mq, a.phq, a.F, a.L, c.BH) || !map_rows(&mk, a.phk, a.F, a.L, c.BH) || !map_rows(&mv, a.v, 64, a.L, c.BH))
         return cudaErrorInvalidValue;
     P p = base(a, c, err);
-    cudaError_t e = segment_states(a, c, k, p, mk, mv, false, a.S_in, a.z_in, a.S_out, a.z_out, st);
+    bool chained = false;   // whether a kernel of this call runs before
+    cudaError_t e = segment_states(a, c, k, p, mk, mv, false, a.S_in, a.z_in, a.S_out, a.z_out, chained, st);
     if (e != cudaSuccess) return e;
     if (c.nseg == 1) {
         p.last = a.S_out;
@@ -1195,7 +1199,7 @@ cudaError_t decay_tc_fwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
     }
     p.o = static_cast<__nv_bfloat16*>(a.out_w);
     p.den = a.den_w;
-    return out_f(mk, mq, mv, p, c, k, false, a.norm, st);
+    return out_f(mk, mq, mv, p, c, k, false, a.norm, chained, st);
 }
 
 cudaError_t decay_tc_bwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st)
@@ -1207,28 +1211,29 @@ cudaError_t decay_tc_bwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
         !map_rows(&mv, a.v, 64, a.L, c.BH) || !map_rows(&mo, a.dout, 64, a.L, c.BH) ||
         !map_rows(&mdq, a.dphq, a.F, a.L, c.BH, true) || !map_rows(&mdk, a.dphk, a.F, a.L, c.BH, true))
         return cudaErrorInvalidValue;
+    bool chained = a.norm;   // whether a kernel of this call runs before
     cudaError_t e = a.norm ? decay_row_stats(a, k.rz, k.r, st) : cudaSuccess;
     if (e != cudaSuccess) return e;
     const float *rz = a.norm ? k.rz : nullptr, *r = a.norm ? k.r : nullptr;
     P s = base(a, cq, err);   // dphq from the states before each token
-    if ((e = segment_states(a, cq, k, s, mk, mv, false, a.S_in, a.z_in, nullptr, nullptr, st)) != cudaSuccess) return e;
+    if ((e = segment_states(a, cq, k, s, mk, mv, false, a.S_in, a.z_in, nullptr, nullptr, chained, st)) != cudaSuccess) return e;
     s.q_mul = rz;
     s.q_off = r;
     s.o = static_cast<__nv_bfloat16*>(a.dphq);
-    if ((e = launch<kOutE>("tc_decay_out_e", mk, mk, mv, mo, mdq, s, cq, false, a.norm, st)) != cudaSuccess) return e;
+    if ((e = launch<kOutE>("tc_decay_out_e", mk, mk, mv, mo, mdq, s, cq, false, a.norm, chained, st)) != cudaSuccess) return e;
     P g = base(a, c, err);   // dphk and dv from the states after each token
     g.s_mul = rz;
     g.s_off = r;
-    if ((e = segment_states(a, c, k, g, mq, mo, true, a.dS_out, a.dz_out, a.dS_in, a.dz_in, st)) != cudaSuccess) return e;
+    if ((e = segment_states(a, c, k, g, mq, mo, true, a.dS_out, a.dz_out, a.dS_in, a.dz_in, chained, st)) != cudaSuccess) return e;
     g.o = static_cast<__nv_bfloat16*>(a.dphk);
-    if ((e = launch<kOutE>("tc_decay_out_e", mq, mq, mo, mv, mdk, g, c, true, a.norm, st)) != cudaSuccess) return e;
+    if ((e = launch<kOutE>("tc_decay_out_e", mq, mq, mo, mv, mdk, g, c, true, a.norm, chained, st)) != cudaSuccess) return e;
     if (c.nseg == 1) {       // (the sweep that writes over dS_out when dS_in is dS_out: the last one)
         g.last = a.dS_in;
         g.last_z = a.dz_in;
         g.z_state = a.dz_in != nullptr;
     }
     g.o = static_cast<__nv_bfloat16*>(a.dv);
-    return out_f(mq, mk, mo, g, c, k, true, a.norm, st);
+    return out_f(mq, mk, mo, g, c, k, true, a.norm, chained, st);
 }
 
 }  // namespace slay
