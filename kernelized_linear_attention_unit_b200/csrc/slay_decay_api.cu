@@ -30,8 +30,8 @@ slay_status check_sizes(int B, int H, int L, int F, int Dv, slay_dtype dt, bool 
     if (B < 0 || H < 0 || L < 0 || F <= 0 || Dv <= 0) return SLAY_ERR_INVALID_ARG;
     if (Dv != kD || F > kMaxF) return SLAY_ERR_UNSUPPORTED;
     if (!dtype_ok(dt) || (norm && !eps_ok(eps))) return SLAY_ERR_INVALID_ARG;
-    // grid limits of the launches: (b, h) indexes grid y / z, as in the other entry points
-    if (static_cast<int64_t>(B) * H > 65535 || (static_cast<int64_t>(L) + 63) / 64 > 65535)
+    // grid limits of the launches: (b, h), up to three times, indexes grid y / z
+    if (static_cast<int64_t>(B) * H > 65535 / 3 || (static_cast<int64_t>(L) + 63) / 64 > 65535)
         return SLAY_ERR_UNSUPPORTED;
     return SLAY_OK;
 }

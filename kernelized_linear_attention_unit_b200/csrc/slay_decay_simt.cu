@@ -6,8 +6,8 @@
 // as 4 x 4 fp32 accumulators per thread, operands in shared memory as fp32:
 //   k_dec_state : each chunk's own state  T = sum_j w_j y_j u_j^T  (a CTA per 64 features)
 //   k_dec_scan  : the states entering each chunk, M <- lambda^n M + T, one thread per element
-//   k_dec_out_f : queries on the F side (out, dv), outputs 64 wide
-//   k_dec_out_e : queries on the E side (dphq, dphk), outputs F wide, 64 columns at a time
+//   k_dec_fwd, k_dec_grads : the outputs, per chunk out_f (queries on the F side: out, dv;
+//                 64 wide) or out_e (queries on the E side: dphq, dphk; F wide, 64 at a time)
 // fp32 FMA bounds them (per token and head about 2 (3 * 64 F + 64 * 64) operations per sweep
 // against 8 F + 512 bytes); 64-token chunks keep the quadratic part below the state part for
 // every F >= 64.
@@ -51,6 +51,8 @@ __device__ __forceinline__ void st4(__nv_bfloat16* p, float4 x)
 
 // A sweep's operands (see slay_decay.h); null scalars stand for 1 (mul) and 0 (off).
 struct Sweep {
+    const float *first, *first_z;   // the state entering the walk (null: zero)
+    float *last, *last_z;           // the one leaving it (null: not wanted)
     const void* fs;       // F side of the state [BH][L][F]
     const void* es;       // E side of the state [BH][L][64]
     const void* fq;       // query, F side (out, dv)
@@ -157,16 +159,17 @@ __device__ __forceinline__ float state_weight(float g2, int j, int n, bool rev)
 }
 
 // ------------------------------------------------------------------ chunk states
-// grid (nc, ceil(F / 64), BH)
+// grid (nc, ceil(F / 64), BH, or 2 BH with a second sweep)
 template <typename T>
-__global__ void __launch_bounds__(kNT) k_dec_state(Sweep s)
+__global__ void __launch_bounds__(kNT) k_dec_state(Sweep s0, Sweep s1, int BH)
 {
+    const Sweep& s = static_cast<int>(blockIdx.z) < BH ? s0 : s1;
     extern __shared__ __align__(16) float sm[];
     float* fsm = sm;                    // [64 j][f]
     float* esm = sm + 64 * kPitch;      // [64 j][e], weighted
     __shared__ float w[kC], wz[kC];
     const int c = blockIdx.x, f0 = blockIdx.y * 64;
-    const int64_t bh = blockIdx.z;
+    const int64_t bh = static_cast<int>(blockIdx.z) % BH;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int t0 = c * kC, n = min(kC, seq_len(s.lengths, static_cast<int>(bh / s.H), s.L) - t0);
     const float g2 = s.log_decay[bh % s.H] * kLog2e;
@@ -217,13 +220,13 @@ __global__ void __launch_bounds__(kNT) k_dec_state(Sweep s)
 // Chunk states -> the state entering each chunk (in place), S and z in one launch; first: the
 // state entering the walk (null: zero), last: the one leaving it (null: not wanted; may be
 // `first` itself, each element is read before it is written).  Loads run eight chunks ahead.
-// grid (ceil(64 F / 4 kNT) + ceil(F / kNT), BH): a thread has four elements of S or one of z
+// grid (ceil(64 F / 4 kNT) + ceil(F / kNT), BH, or 2 BH with a second sweep): a thread has four elements of S or one of z
 // (whose rows need not be whole float4s).
-__global__ void __launch_bounds__(kNT) k_dec_scan(Sweep s, const float* first, const float* first_z, float* last,
-                                                  float* last_z, int s_blocks)
+__global__ void __launch_bounds__(kNT) k_dec_scan(Sweep s0, Sweep s1, int BH, int s_blocks)
 {
     after_previous_kernel();
-    const int64_t bh = blockIdx.y;
+    const Sweep& s = static_cast<int>(blockIdx.y) < BH ? s0 : s1;
+    const int64_t bh = static_cast<int>(blockIdx.y) % BH;
     const int n = seq_len(s.lengths, static_cast<int>(bh / s.H), s.L);
     const float g2 = s.log_decay[bh % s.H] * kLog2e;
     const float lam_c = decay_pow(g2, kC);
@@ -250,13 +253,13 @@ __global__ void __launch_bounds__(kNT) k_dec_scan(Sweep s, const float* first, c
     if (static_cast<int>(blockIdx.x) < s_blocks) {
         const int64_t x = static_cast<int64_t>(blockIdx.x) * kNT + threadIdx.x, w = static_cast<int64_t>(s.F) * 16;
         if (x < w)
-            walk(reinterpret_cast<float4*>(s.st), reinterpret_cast<const float4*>(first), reinterpret_cast<float4*>(last), w, x,
+            walk(reinterpret_cast<float4*>(s.st), reinterpret_cast<const float4*>(s.first), reinterpret_cast<float4*>(s.last), w, x,
                  make_float4(0.f, 0.f, 0.f, 0.f), [](float l, float4 a, float4 b) {
                      return make_float4(fmaf(l, a.x, b.x), fmaf(l, a.y, b.y), fmaf(l, a.z, b.z), fmaf(l, a.w, b.w));
                  });
     } else {
         const int64_t x = static_cast<int64_t>(blockIdx.x - s_blocks) * kNT + threadIdx.x;
-        if (x < s.F) walk(s.sz, first_z, last_z, s.F, x, 0.0f, [](float l, float a, float b) { return fmaf(l, a, b); });
+        if (x < s.F) walk(s.sz, s.first_z, s.last_z, s.F, x, 0.0f, [](float l, float a, float b) { return fmaf(l, a, b); });
     }
 }
 
@@ -269,17 +272,14 @@ __device__ __forceinline__ float score(float raw, int i, int j, int n, bool rev,
 }
 
 // ----------------------------------------------------- outputs 64 wide (out, dv)
-// grid (nc, BH)
 template <typename T>
-__global__ void __launch_bounds__(kNT) k_dec_out_f(Sweep s, T* o, float* den, bool norm, float eps)
+__device__ __forceinline__ void out_f(const Sweep& s, float* sm, int64_t bh, T* o, float* den, bool norm, float eps)
 {
-    extern __shared__ __align__(16) float sm[];
     float* fqs = sm;                        // [64 i][64 f]
     float* fss = fqs + 64 * kPitch;         // [64 j][64 f]; then the scores [64 i][64 j]
     float* ms = fss + 64 * kPitch;          // [64 f][64 e]; then the E side [64 j][64 e]
     __shared__ float pw[kC], smul[kC], zs[64], dsum[kC];
     const int c = blockIdx.x;
-    const int64_t bh = blockIdx.y;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int t0 = c * kC, n = min(kC, seq_len(s.lengths, static_cast<int>(bh / s.H), s.L) - t0);
     after_previous_kernel();
@@ -356,18 +356,15 @@ __global__ void __launch_bounds__(kNT) k_dec_out_f(Sweep s, T* o, float* den, bo
 }
 
 // ----------------------------------------------------- outputs F wide (dphq, dphk)
-// grid (nc, BH, column groups)
 template <typename T>
-__global__ void __launch_bounds__(kNT) k_dec_out_e(Sweep s, T* o, bool norm)
+__device__ __forceinline__ void out_e(const Sweep& s, float* sm, int64_t bh, T* o, bool norm)
 {
-    extern __shared__ __align__(16) float sm[];
     float* eqs = sm;                        // [64 i][64 e]
     float* ps = eqs + 64 * kPitch;          // E side of the state, then the scores [64 i][64 j]
     float* fss = ps + 64 * kPitch;          // [64 j][64 f]
     float* ms = fss + 64 * kPitch;          // [64 f][64 e]
     __shared__ float pw[kC], smul[kC], soff[kC], zs[64];
     const int c = blockIdx.x;
-    const int64_t bh = blockIdx.y;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int t0 = c * kC, n = min(kC, seq_len(s.lengths, static_cast<int>(bh / s.H), s.L) - t0);
     after_previous_kernel();
@@ -439,6 +436,24 @@ __global__ void __launch_bounds__(kNT) k_dec_out_e(Sweep s, T* o, bool norm)
     }
 }
 
+// grid (nc, BH)
+template <typename T>
+__global__ void __launch_bounds__(kNT) k_dec_fwd(Sweep s, T* o, float* den, bool norm, float eps)
+{
+    extern __shared__ __align__(16) float sm[];
+    out_f(s, sm, blockIdx.y, o, den, norm, eps);
+}
+
+// The three gradients side by side: grid (nc, 3 BH, column groups of the F-wide ones)
+template <typename T>
+__global__ void __launch_bounds__(kNT) k_dec_grads(Sweep s, Sweep g, T* dphq, T* dphk, T* dv, int BH, bool norm)
+{
+    extern __shared__ __align__(16) float sm[];
+    const int role = blockIdx.y / BH, bh = blockIdx.y % BH;
+    if (role < 2) out_e(role ? g : s, sm, bh, role ? dphk : dphq, norm);
+    else if (blockIdx.z == 0) out_f<T>(g, sm, bh, dv, nullptr, false, 0.0f);
+}
+
 // Row statistics of the normalized backward: 16 bytes a lane, so 8 (bf16) or 16 (fp32) lanes a
 // row; bound by the reads of out and dout.
 template <typename T>
@@ -471,36 +486,34 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 constexpr size_t kSmemF = 3 * 64 * kPitch * sizeof(float), kSmemE = 4 * 64 * kPitch * sizeof(float),
                  kSmemS = 2 * 64 * kPitch * sizeof(float);
 
+// The states of a sweep, or of two at once.
 template <typename T>
-cudaError_t states(const Sweep& s, int64_t BH, const float* first, const float* first_z, float* last, float* last_z,
-                   bool& chained, cudaStream_t st)
+cudaError_t states(const Sweep& s, const Sweep* g, int BH, bool chained, cudaStream_t st)
 {
-    cudaError_t e = cudaSuccess;
+    const unsigned n = g ? 2 * BH : BH;
     if (s.nc > 0) {   // L == 0: the walk has no chunk and hands its state on
         TraceScope trace_("simt_decay_state", st);
-        e = launch_in_chain(!chained, k_dec_state<T>, dim3(s.nc, (s.F + 63) / 64, static_cast<unsigned>(BH)), kNT, kSmemS, st, s);
-        chained = true;
+        const cudaError_t e = launch_in_chain(!chained, k_dec_state<T>, dim3(s.nc, (s.F + 63) / 64, n), kNT, kSmemS, st, s,
+                                              g ? *g : s, BH);
         if (e != cudaSuccess) return e;
+        chained = true;
     }
     const int sb = (s.F * 16 + kNT - 1) / kNT, zb = s.sz ? (s.F + kNT - 1) / kNT : 0;
     TraceScope trace_("simt_decay_scan", st);
-    e = launch_in_chain(!chained, k_dec_scan, dim3(sb + zb, static_cast<unsigned>(BH)), kNT, 0, st, s, first, first_z, last,
-                        last_z, sb);
-    chained = true;
-    return e;
+    return launch_in_chain(!chained, k_dec_scan, dim3(sb + zb, n), kNT, 0, st, s, g ? *g : s, BH, sb);
 }
 
 template <typename T>
 cudaError_t prepare_smem()
 {
-    cudaError_t e = cudaFuncSetAttribute(k_dec_out_f<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemF);
+    cudaError_t e = cudaFuncSetAttribute(k_dec_fwd<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemF);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_dec_out_e<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemE);
+        e = cudaFuncSetAttribute(k_dec_grads<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemE);
     return e;
 }
 
 struct Carve {
-    float *st, *sz, *rz, *r;
+    float *st, *sz, *gt, *gz, *rz, *r;
     size_t bytes;
 };
 
@@ -518,6 +531,8 @@ Carve carve(const DecayArgs& a, bool bwd, void* ws)
     c.st = take(static_cast<size_t>(BH) * nc * a.F * 64);
     c.sz = take(static_cast<size_t>(BH) * nc * a.F);
     if (bwd) {
+        c.gt = take(static_cast<size_t>(BH) * nc * a.F * 64);
+        c.gz = take(static_cast<size_t>(BH) * nc * a.F);
         c.rz = take(static_cast<size_t>(BH) * a.L);
         c.r = take(static_cast<size_t>(BH) * a.L);
     }
@@ -543,47 +558,44 @@ template <typename T>
 cudaError_t fwd_t(const DecayArgs& a, void* ws, cudaStream_t st)
 {
     const Carve c = carve(a, false, ws);
-    const int64_t BH = static_cast<int64_t>(a.B) * a.H;
+    const int BH = a.B * a.H;
     cudaError_t e = prepare_smem<T>();
     if (e != cudaSuccess) return e;
-    bool chained = false;   // whether a kernel of this call runs before
     Sweep s = base(a, c);
     s.fq = a.phq;
     s.fs = a.phk;
     s.es = a.v;
-    if ((e = states<T>(s, BH, a.S_in, a.z_in, a.S_out, a.z_out, chained, st)) != cudaSuccess || s.nc == 0) return e;
+    s.first = a.S_in;
+    s.first_z = a.z_in;
+    s.last = a.S_out;
+    s.last_z = a.z_out;
+    if ((e = states<T>(s, nullptr, BH, false, st)) != cudaSuccess || s.nc == 0) return e;
     TraceScope trace_("simt_decay_out", st);
-    return launch_in_chain(false, k_dec_out_f<T>, dim3(s.nc, static_cast<unsigned>(BH)), kNT, kSmemF, st, s,
-                           static_cast<T*>(a.out_w), a.den_w, a.norm, a.eps);
+    return launch_in_chain(false, k_dec_fwd<T>, dim3(s.nc, BH), kNT, kSmemF, st, s, static_cast<T*>(a.out_w), a.den_w, a.norm,
+                           a.eps);
 }
 
 template <typename T>
 cudaError_t bwd_t(const DecayArgs& a, void* ws, cudaStream_t st)
 {
     const Carve c = carve(a, true, ws);
-    const int64_t BH = static_cast<int64_t>(a.B) * a.H;
+    const int BH = a.B * a.H;
     cudaError_t e = prepare_smem<T>();
     if (e != cudaSuccess) return e;
-    if (a.norm && a.L > 0 && (e = decay_row_stats(a, c.rz, c.r, st)) != cudaSuccess) return e;
-    bool chained = a.norm && a.L > 0;   // whether a kernel of this call runs before
+    const bool stats = a.norm && a.L > 0;
+    if (stats && (e = decay_row_stats(a, c.rz, c.r, st)) != cudaSuccess) return e;
     const float *rz = a.norm ? c.rz : nullptr, *r = a.norm ? c.r : nullptr;
-    // few CTAs: the column blocks of the F-wide outputs go to CTAs of their own
-    const int nfb = (a.F + 63) / 64, nc = (a.L + kC - 1) / kC;
-    const int zsplit = nc == 0 || nc * BH >= 296 ? 1 : std::min<int64_t>(nfb, (296 + nc * BH - 1) / (nc * BH));
-    Sweep s = base(a, c);   // dphq from the forward states
+    Sweep s = base(a, c);   // dphq from the states before each token
     s.fs = a.phk;
     s.es = a.v;
     s.eq = a.dout;
     s.q_mul = rz;
     s.q_off = r;
-    if (nc > 0) {
-        if ((e = states<T>(s, BH, a.S_in, a.z_in, nullptr, nullptr, chained, st)) != cudaSuccess) return e;
-        TraceScope trace_("simt_decay_out", st);
-        e = launch_in_chain(false, k_dec_out_e<T>, dim3(nc, static_cast<unsigned>(BH), zsplit), kNT, kSmemE, st, s,
-                            static_cast<T*>(a.dphq), a.norm);
-        if (e != cudaSuccess) return e;
-    }
-    Sweep g = base(a, c);   // dphk and dv from the backward states
+    s.first = a.S_in;
+    s.first_z = a.z_in;
+    Sweep g = base(a, c);   // dphk and dv from the states after each token
+    g.st = c.gt;
+    g.sz = a.norm ? c.gz : nullptr;
     g.rev = true;
     g.fs = a.phq;
     g.es = a.dout;
@@ -592,13 +604,19 @@ cudaError_t bwd_t(const DecayArgs& a, void* ws, cudaStream_t st)
     g.z_delta = a.norm;
     g.eq = a.v;
     g.fq = a.phk;
-    if ((e = states<T>(g, BH, a.dS_out, a.dz_out, a.dS_in, a.dz_in, chained, st)) != cudaSuccess || nc == 0) return e;
+    g.first = a.dS_out;
+    g.first_z = a.dz_out;
+    g.last = a.dS_in;
+    g.last_z = a.dz_in;
+    if (s.nc == 0) return states<T>(g, nullptr, BH, false, st);
+    if ((e = states<T>(s, &g, BH, stats, st)) != cudaSuccess) return e;
+    // few CTAs: the column blocks of the F-wide outputs go to CTAs of their own
+    const int nfb = (a.F + 63) / 64;
+    const int64_t ctas = 3 * static_cast<int64_t>(BH) * s.nc;
+    const int zsplit = static_cast<int>(ctas >= 296 ? 1 : std::min<int64_t>(nfb, (296 + ctas - 1) / ctas));
     TraceScope trace_("simt_decay_out", st);
-    e = launch_in_chain(false, k_dec_out_e<T>, dim3(nc, static_cast<unsigned>(BH), zsplit), kNT, kSmemE, st, g,
-                        static_cast<T*>(a.dphk), a.norm);
-    if (e != cudaSuccess) return e;
-    return launch_in_chain(false, k_dec_out_f<T>, dim3(nc, static_cast<unsigned>(BH)), kNT, kSmemF, st, g, static_cast<T*>(a.dv),
-                           nullptr, false, 0.0f);
+    return launch_in_chain(false, k_dec_grads<T>, dim3(s.nc, 3 * BH, zsplit), kNT, kSmemE, st, s, g, static_cast<T*>(a.dphq),
+                           static_cast<T*>(a.dphk), static_cast<T*>(a.dv), BH, a.norm);
 }
 
 }  // namespace

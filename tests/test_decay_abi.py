@@ -47,11 +47,11 @@ def _copy(**kw):
 
 
 SIZES = [(dict(B=-1), BAD), (dict(L=-1), BAD), (dict(F=0), BAD), (dict(F=1025), NO), (dict(Dv=128), NO), (dict(dt=2), BAD),
-         (dict(eps=0.0), BAD), (dict(eps=float("nan")), BAD), (dict(B=70000, H=1), NO), (dict(log_decay=None), BAD),
+         (dict(eps=0.0), BAD), (dict(eps=float("nan")), BAD), (dict(B=22000, H=1), NO), (dict(log_decay=None), BAD),
          (dict(log_decay=P + 2), BAD), (dict(lengths=P + 1), BAD), (dict(phq=None), BAD), (dict(phk=P + 8), BAD),
          (dict(v=None), BAD), (dict(S_in=P), BAD), (dict(z_in=P), BAD), (dict(S_in=P, z_in=P + 4), BAD),
          (dict(S_in=P, z_in=P, normalize=0, den=None), BAD), (dict(ws=None), BAD), (dict(ws=P + 128), BAD),
-         (dict(ws_bytes=1000), BAD), (dict(B=0), OK), (dict(H=0), OK), (dict(L=0), OK)]
+         (dict(ws_bytes=100), BAD), (dict(B=0), OK), (dict(H=0), OK), (dict(L=0), OK)]
 
 
 @pytest.mark.parametrize("kw,want", SIZES + [(dict(out=None), BAD), (dict(den=P + 1), BAD), (dict(normalize=0), BAD),
