@@ -59,8 +59,8 @@ __host__ __device__ constexpr int threads(int mode) { return 32 * (split(mode) ?
 // takes the other 64.  T of 128 features: the first limb's 64 columns, in the modes with
 // room a second limb's, and 16 for z.
 constexpr uint32_t kColP = 0, kColOi = 64, kColOe = 128, kColDen = 192;
-// kOutE: two output buffers; the first limb's form puts the second one's Oi over the scores,
-// the two-limb form (128 features) has room beside them
+// kOutE: two output buffers; the one-limb form puts the second one's Oi over the scores, the
+// two-limb form (128 features) has room beside them
 __host__ __device__ constexpr uint32_t col_oi(bool limbs, int b) { return limbs ? 128 + 128 * b : b ? 64 : 128; }
 __host__ __device__ constexpr uint32_t col_oe(bool limbs, int b) { return limbs ? 192 + 128 * b : b ? 256 : 192; }
 __host__ __device__ constexpr uint32_t col_t(int mode, bool limbs) { return limbs ? 384 : mode == kOutE ? 352 : 208; }
@@ -101,18 +101,30 @@ __host__ __device__ constexpr Layout layout(int mode)
     return l;
 }
 
+// The segments' sums and starting states, private to a call: per (b, h, segment) the float4s
+// [128 features][16 of a row][128 rows], in the order in which a warp reads and writes them.
+__host__ __device__ __forceinline__ int64_t sums_floats(int F) { return static_cast<int64_t>((F + 127) / 128) * 128 * 64; }
+__device__ __forceinline__ int64_t sums_at(int f, int e4)   // in float4s
+{
+    return (static_cast<int64_t>(f >> 7) * 16 + e4) * 128 + (f & 127);
+}
+
 struct P {
     const float* log_decay;
     const int32_t* lengths;
     const float *s_mul, *s_off, *q_mul, *q_off;   // row scalars, null: 1 / 0
-    const float *first, *first_z;                 // states entering: [BH][nseg] (or [BH]), null: zero
-    float *last, *last_z;                         // states leaving, likewise, null: not wanted
+    const float *first, *first_z;                 // states entering the walk [BH], null: zero
+    const float *sums, *sums_z;                   // the segments' own sums [BH][nseg]: a sweep adds up those
+                                                  // before its segment; null: one segment, or
+    const float *starts, *starts_z;               // the states entering the segments [BH][nseg]
+    float *last, *last_z;                         // states leaving: the walk [BH]; kState: the sums [BH][nseg]
     __nv_bfloat16* o;
     float* den;
-    float *part, *part_den;                       // numerators and denominators over features [BH][L][64], [BH][L]
+    float *part, *part_den;                       // numerators and denominators over features, by chunk
     int part_mode;                                // 0: none, 1: store them, 2: add them to this block's
     float eps;
     int H, L, F, nseg, nfb, fw, fb0;
+    int seg0, nsl;                                // segments of this launch: seg0 .. seg0 + nsl - 1
     int z_state;                                  // keep z (kOutF backward: only where it is wanted)
     int* err;
 };
@@ -193,19 +205,21 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     int x = blockIdx.x;
     const int fb = kMode == kOutF ? p.fb0 : x % p.nfb;
     if (kMode != kOutF) x /= p.nfb;
-    const int seg = x % p.nseg, bh = x / p.nseg;
+    const int seg = p.seg0 + x % p.nsl, bh = x / p.nsl;
     const int f0 = fb * p.fw, fv = min(p.fw, p.F - f0);
     const int ns = (fv + 63) >> 6, nsE = (ns + 1) & ~1;   // 64-feature slices; as whole pairs
     const int len = p.lengths ? min(max(p.lengths[bh / p.H], 0), p.L) : p.L;
     const int nch = (len + kT - 1) / kT;
-    const int c_lo = seg * nch / p.nseg;                  // (at most 32768 chunks, 148 segments)
-    const int count = (seg + 1) * nch / p.nseg - c_lo;
+    auto seg_lo = [&](int s) { return s * nch / p.nseg; };   // (at most 32768 chunks, 148 segments)
+    const int c_lo = seg_lo(seg), count = seg_lo(seg + 1) - c_lo;
+    // whether the state that leaves this CTA's walk is an output
+    const bool leaves = p.last && (kMode == kState || seg == (kRev ? 0 : p.nseg - 1));
     auto chunk_of = [&](int i) { return kRev ? c_lo + count - 1 - i : c_lo + i; };
     const float g2 = p.log_decay[bh % p.H] * kLog2e;
     // limbs of the weighted rows: three where the fp32 state leaves the call, two (2^-17) where
     // only its bf16 copy is read; without decay and row scalars the weights are 1, one is exact
     const bool has_z = kNorm && (kMode != kOutF || !kRev || p.z_state);
-    const int nl = g2 == 0.0f && !kCols ? 1 : (kMode == kState || (kMode == kOutF && p.last)) ? 3 : 2;
+    const int nl = g2 == 0.0f && !kCols ? 1 : (kMode == kState || (kMode == kOutF && leaves)) ? 3 : 2;
 
     // kOutF: limb tiles 0, 1 at y + 16 KiB, 2 at y, which is the query ring's fourth slot otherwise
     const int nfq = nl == 3 ? 3 : 4;
@@ -659,22 +673,40 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
         regs_inc<kSplit ? 192 : 208>();
         float run[2][kW], zrun[2] = {0.0f, 0.0f};   // M at (f = 128 b + row, e = 32 half + c); z at b
         auto has_zrow = [&](int b) { return has_z && (kSplit || b == half); };
-        {
+        // the state entering the segment: M <- lambda^n M + (its sums) over the segments before it
+        auto add_state = [&](const float* S, const float* z, int64_t at, float lam, bool own) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const int f = 128 * b + row;
-                const bool in = p.first && f < fv;
-                const float4* src = reinterpret_cast<const float4*>(p.first + ((sidx * p.F) + f0 + f) * 64 + 32 * half);
+                if (f >= fv) continue;
+                const float4* src = own ? reinterpret_cast<const float4*>(S + at * sums_floats(p.F)) + sums_at(f0 + f, 8 * half)
+                                        : reinterpret_cast<const float4*>(S + (at * p.F + f0 + f) * 64 + 32 * half);
+                const int step = own ? 128 : 1;
 #pragma unroll
                 for (int c = 0; c < kW / 4; ++c) {
-                    const float4 w = in ? src[c] : make_float4(0.f, 0.f, 0.f, 0.f);
-                    run[b][4 * c] = w.x;
-                    run[b][4 * c + 1] = w.y;
-                    run[b][4 * c + 2] = w.z;
-                    run[b][4 * c + 3] = w.w;
+                    const float4 w = src[c * step];
+                    run[b][4 * c] = fmaf(lam, run[b][4 * c], w.x);
+                    run[b][4 * c + 1] = fmaf(lam, run[b][4 * c + 1], w.y);
+                    run[b][4 * c + 2] = fmaf(lam, run[b][4 * c + 2], w.z);
+                    run[b][4 * c + 3] = fmaf(lam, run[b][4 * c + 3], w.w);
                 }
-                if (in && has_zrow(b)) zrun[b] = p.first_z[sidx * p.F + f0 + f];
+                if (has_zrow(b)) zrun[b] = fmaf(lam, zrun[b], z[at * p.F + f0 + f]);
             }
+        };
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int c = 0; c < kW; ++c) run[b][c] = 0.0f;
+        if (p.starts) {
+            add_state(p.starts, p.starts_z, sidx, 1.0f, true);
+        } else {
+            if (p.first) add_state(p.first, p.first_z, bh, 1.0f, false);
+            if (p.sums)
+                for (int i = 0; i < (kRev ? p.nseg - 1 - seg : seg); ++i) {
+                    const int s = kRev ? p.nseg - 1 - i : i;
+                    add_state(p.sums, p.sums_z, static_cast<int64_t>(bh) * p.nseg + s,
+                              decay_pow(g2, max(min(seg_lo(s + 1) * kT, len) - seg_lo(s) * kT, 0)), true);
+                }
         }
         // the operand copy of M, and its z column, for chunk i
         auto write_m = [&](int i) {
@@ -855,6 +887,18 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 const bool valid = row < n;
                 const float fac = decay_pow(g2, kRev ? max(n - 1 - row, 0) : row + 1);
                 scores(i, 0.0f, 1.0f);
+                // the earlier feature blocks' sums: [chunk][16 float4 of a row][128 rows], so that a
+                // warp's accesses are whole lines; on their way while the state is summed
+                const int64_t pc = static_cast<int64_t>(bh) * ((p.L + kT - 1) / kT) + chunk_of(i);
+                float4* pp = reinterpret_cast<float4*>(p.part) + (pc * 16 + 8 * half) * kT + row;
+                float* pd = p.part_den + pc * kT + row;
+                float4 part[8];
+                float part_dn = 0.0f;
+                if (p.part_mode == 2) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) part[c] = pp[c * kT];
+                    if (kDen) part_dn = *pd;
+                }
                 update_m(i);
                 if (more) write_m(i + 1);   // the next chunk's products want the state first
                 wait_k(B_OF, i);
@@ -881,23 +925,19 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 if (kDen)
                     dn = fmaf(fac, __uint_as_float(d0) + (__uint_as_float(d1) + __uint_as_float(d2)),
                               dsum[par * 2 * kT + row] + dsum[(par * 2 + 1) * kT + row]);
-                if (p.part_mode && valid) {
-                    float4* pp = reinterpret_cast<float4*>(p.part + grow * 64 + 32 * half);
-                    if (p.part_mode == 1) {
+                if (p.part_mode == 1) {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) pp[c] = make_float4(t[4 * c], t[4 * c + 1], t[4 * c + 2], t[4 * c + 3]);
-                        if (half == 0) p.part_den[grow] = dn;
-                    } else {
+                    for (int c = 0; c < 8; ++c) pp[c * kT] = make_float4(t[4 * c], t[4 * c + 1], t[4 * c + 2], t[4 * c + 3]);
+                    if (half == 0) *pd = dn;
+                } else if (p.part_mode == 2) {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const float4 w = pp[c];
-                            t[4 * c] += w.x;
-                            t[4 * c + 1] += w.y;
-                            t[4 * c + 2] += w.z;
-                            t[4 * c + 3] += w.w;
-                        }
-                        dn += p.part_den[grow];
+                    for (int c = 0; c < 8; ++c) {
+                        t[4 * c] += part[c].x;
+                        t[4 * c + 1] += part[c].y;
+                        t[4 * c + 2] += part[c].z;
+                        t[4 * c + 3] += part[c].w;
                     }
+                    dn += part_dn;
                 }
                 if (p.part_mode != 1) {
                     if (kDen) {
@@ -933,16 +973,18 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 if (more) write_y(i + 1);
             }
         }
-        if (p.last) {
+        if (leaves) {
+            const int64_t at = kMode == kState ? sidx : bh;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const int f = 128 * b + row;
                 if (f >= fv) continue;
-                float4* dst = reinterpret_cast<float4*>(p.last + ((sidx * p.F) + f0 + f) * 64 + 32 * half);
+                float4* dst = kMode == kState ? reinterpret_cast<float4*>(p.last + at * sums_floats(p.F)) + sums_at(f0 + f, 8 * half)
+                                              : reinterpret_cast<float4*>(p.last + (at * p.F + f0 + f) * 64 + 32 * half);
 #pragma unroll
                 for (int c = 0; c < kW / 4; ++c)
-                    dst[c] = make_float4(run[b][4 * c], run[b][4 * c + 1], run[b][4 * c + 2], run[b][4 * c + 3]);
-                if (has_zrow(b) && p.last_z) p.last_z[sidx * p.F + f0 + f] = zrun[b];
+                    dst[c * (kMode == kState ? 128 : 1)] = make_float4(run[b][4 * c], run[b][4 * c + 1], run[b][4 * c + 2], run[b][4 * c + 3]);
+                if (has_zrow(b) && p.last_z) p.last_z[at * p.F + f0 + f] = zrun[b];
             }
         }
         }
@@ -954,9 +996,10 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Segment sums -> the states entering the segments, in place, S and z in one launch, four
-// elements a thread; first and last as in k_dec_scan.  Loads run eight segments ahead of the
-// stores (L2 latency would be paid per segment otherwise).  grid (ceil(F * 65 / 1024), BH)
+// Segment sums -> the states entering the segments, in place, S (four elements a thread) and z
+// in one launch; first: the state entering the walk (null: zero), last: the one leaving it
+// (null: not wanted; may be first).  Loads run eight segments ahead of the stores (L2 latency
+// would be paid per segment otherwise).  grid (ceil((sums_floats(F) / 4 + F) / 256), BH)
 __global__ void __launch_bounds__(256) k_dec_seg_scan(float* st, float* sz, const float* first, const float* first_z,
                                                       float* last, float* last_z, int F, int nseg, bool rev,
                                                       const float* log_decay, const int32_t* lengths, int H, int L)
@@ -972,34 +1015,40 @@ __global__ void __launch_bounds__(256) k_dec_seg_scan(float* st, float* sz, cons
     }
     after_previous_kernel();
     __syncthreads();
-    int x = (blockIdx.x * 256 + threadIdx.x) * 4;
-    int64_t w = static_cast<int64_t>(F) * 64;
-    if (x >= w) {
-        x -= static_cast<int>(w);
-        w = F;
-        if (!sz || x >= F) return;   // (F % 8 == 0: whole float4s)
-        st = sz;
-        first = first_z;
-        last = last_z;
-    }
-    float4 run = first ? *reinterpret_cast<const float4*>(first + bh * w + x) : make_float4(0.f, 0.f, 0.f, 0.f);
-    float* q = st + bh * nseg * w + x;
     constexpr int kAhead = 8;
-    for (int i0 = 0; i0 < nseg; i0 += kAhead) {
-        float4 t[kAhead];
+    auto walk = [&](auto* q, int64_t w, auto run, auto* to, auto step) {
+        for (int i0 = 0; i0 < nseg; i0 += kAhead) {
+            decltype(run) t[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (i0 + i < nseg) t[i] = *reinterpret_cast<const float4*>(q + (rev ? nseg - 1 - i0 - i : i0 + i) * w);
+            for (int i = 0; i < kAhead; ++i)
+                if (i0 + i < nseg) t[i] = q[(rev ? nseg - 1 - i0 - i : i0 + i) * w];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (i0 + i >= nseg) break;
-            const int s = rev ? nseg - 1 - i0 - i : i0 + i;
-            *reinterpret_cast<float4*>(q + s * w) = run;
-            const float l = lam[s];
-            run = make_float4(fmaf(l, run.x, t[i].x), fmaf(l, run.y, t[i].y), fmaf(l, run.z, t[i].z), fmaf(l, run.w, t[i].w));
+            for (int i = 0; i < kAhead; ++i) {
+                if (i0 + i >= nseg) break;
+                const int s = rev ? nseg - 1 - i0 - i : i0 + i;
+                q[s * w] = run;
+                run = step(lam[s], run, t[i]);
+            }
         }
+        if (to) *to = run;
+    };
+    const int x = blockIdx.x * 256 + threadIdx.x;
+    const int64_t w = sums_floats(F) / 4;
+    if (x < w) {
+        const int f = ((x >> 7) >> 4) * 128 + (x & 127);
+        if (f >= F) return;
+        const int64_t at = (static_cast<int64_t>(bh) * F + f) * 16 + ((x >> 7) & 15);
+        walk(reinterpret_cast<float4*>(st) + bh * nseg * w + x, w,
+             first ? reinterpret_cast<const float4*>(first)[at] : make_float4(0.f, 0.f, 0.f, 0.f),
+             last ? reinterpret_cast<float4*>(last) + at : nullptr, [](float l, float4 a, float4 b) {
+                 return make_float4(fmaf(l, a.x, b.x), fmaf(l, a.y, b.y), fmaf(l, a.z, b.z), fmaf(l, a.w, b.w));
+             });
+    } else if (sz && x < w + F) {
+        const int f = x - static_cast<int>(w);
+        const int64_t at = static_cast<int64_t>(bh) * F + f;
+        walk(sz + static_cast<int64_t>(bh) * nseg * F + f, F, first_z ? first_z[at] : 0.0f, last_z ? last_z + at : nullptr,
+             [](float l, float a, float b) { return fmaf(l, a, b); });
     }
-    if (last) *reinterpret_cast<float4*>(last + bh * w + x) = run;
 }
 
 // [BH][L][cols] bf16 as a 3-D tensor, boxes of 64 columns x 128 tokens, 128-byte swizzle;
@@ -1070,12 +1119,13 @@ Carve carve(const DecayArgs& a, bool bwd, void* ws)
     const size_t rows = static_cast<size_t>(c.BH) * a.L;
     const int nseg = bwd ? std::max(c.nseg, plan_q(a).nseg) : c.nseg;
     if (nseg > 1) {
-        k.st = take(static_cast<size_t>(c.BH) * nseg * a.F * 64);
+        k.st = take(static_cast<size_t>(c.BH) * nseg * sums_floats(a.F));
         k.sz = take(static_cast<size_t>(c.BH) * nseg * a.F);
     }
     if (c.nfb > 1) {
-        k.part = take(rows * 64);
-        k.part_den = take(rows);
+        const size_t padded = static_cast<size_t>(c.BH) * ((a.L + kT - 1) / kT) * kT;
+        k.part = take(padded * 64);
+        k.part_den = take(padded);
     }
     if (bwd) {
         k.rz = take(rows);
@@ -1094,7 +1144,7 @@ cudaError_t launch1(const CUtensorMap& fs, const CUtensorMap& fq, const CUtensor
     const auto kernel = k_tc_dec<kMode, kRev, kNorm>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t grid = c.BH * p.nseg * (kMode == kOutF ? 1 : p.nfb);
+    const int64_t grid = c.BH * p.nsl * (kMode == kOutF ? 1 : p.nfb);
     const bool first = !chained;
     chained = true;
     return launch_in_chain(first, +kernel, dim3(static_cast<unsigned>(grid)), threads(kMode), smem, st, fs, fq, es, eq, out, p);
@@ -1118,7 +1168,7 @@ P base(const DecayArgs& a, const Plan& c, int* err)
     p.H = a.H;
     p.L = a.L;
     p.F = a.F;
-    p.nseg = c.nseg;
+    p.nseg = p.nsl = c.nseg;
     p.nfb = c.nfb;
     p.fw = c.fw;
     p.eps = a.eps;
@@ -1126,34 +1176,47 @@ P base(const DecayArgs& a, const Plan& c, int* err)
     return p;
 }
 
-// The states entering each segment: from `first` through the segments' own sums; leaves p
-// ready for the output sweeps (the last state written here, or by the sweep that `p.last`
-// is left for when there is one segment).
+// What the output sweeps start from, and the state that the walk leaves.  Up to kMaxSums
+// segments, each sweep adds up the sums of the segments before its own (66 KB each from L2, at
+// F = 256) and the one that walks last writes the state; beyond, and where that state replaces
+// the one that the other CTAs still read, a scan kernel does both.  B200, forward at F = 256:
+// four segments (B4 H8 L2048) 44 us against 47 with the scan, nine (B1 H16 L16384) 137 against
+// 127.
+constexpr int kMaxSums = 4;
 cudaError_t segment_states(const DecayArgs& a, const Plan& c, const Carve& k, P& p, const CUtensorMap& fs,
                            const CUtensorMap& es, bool rev, const float* first, const float* first_z, float* last,
                            float* last_z, bool& chained, cudaStream_t st)
 {
     p.first = first;
     p.first_z = first_z;
+    p.last = last;
+    p.last_z = last_z;
     if (c.nseg == 1) return cudaSuccess;
-    const Plan cs = [&] {   // (the sums themselves go by blocks of 256 whatever the sweep's)
-        Plan x = plan(a, kMaxFw, true);
-        x.nseg = c.nseg;
-        return x;
-    }();
+    const bool scan = c.nseg > kMaxSums || (last && (last == first || (last_z && last_z == first_z)));
     P q = p;
+    const Plan cs = plan(a, kMaxFw, true);   // (the sums go by blocks of 256 whatever the sweep's)
     q.nfb = cs.nfb;
     q.fw = cs.fw;
     q.first = q.first_z = nullptr;
     q.last = k.st;
     q.last_z = k.sz;
+    if (!scan) {                             // nobody adds the last segment's
+        q.nsl = c.nseg - 1;
+        q.seg0 = rev ? 1 : 0;
+    }
     cudaError_t e = launch<kState>("tc_decay_state", fs, fs, es, es, fs, q, cs, rev, a.norm, chained, st);
     if (e != cudaSuccess) return e;
+    if (!scan) {
+        p.sums = k.st;
+        p.sums_z = k.sz;
+        return cudaSuccess;
+    }
     TraceScope trace_("decay_seg_scan", st);
-    e = launch_in_chain(false, k_dec_seg_scan, dim3((a.F * 65 + 1023) / 1024, static_cast<unsigned>(c.BH)), 256, 0, st, k.st,
+    e = launch_in_chain(false, k_dec_seg_scan, dim3(static_cast<unsigned>((sums_floats(a.F) / 4 + a.F + 255) / 256), static_cast<unsigned>(c.BH)), 256, 0, st, k.st,
                         a.norm ? k.sz : nullptr, first, first_z, last, last_z, a.F, c.nseg, rev, a.log_decay, a.lengths, a.H, a.L);
-    p.first = k.st;
-    p.first_z = k.sz;
+    p.starts = k.st;
+    p.starts_z = k.sz;
+    p.last = p.last_z = nullptr;
     return e;
 }
 
@@ -1193,10 +1256,6 @@ cudaError_t decay_tc_fwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
     bool chained = false;   // whether a kernel of this call runs before
     cudaError_t e = segment_states(a, c, k, p, mk, mv, false, a.S_in, a.z_in, a.S_out, a.z_out, chained, st);
     if (e != cudaSuccess) return e;
-    if (c.nseg == 1) {
-        p.last = a.S_out;
-        p.last_z = a.z_out;
-    }
     p.o = static_cast<__nv_bfloat16*>(a.out_w);
     p.den = a.den_w;
     return out_f(mk, mq, mv, p, c, k, false, a.norm, chained, st);
@@ -1225,13 +1284,11 @@ cudaError_t decay_tc_bwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
     g.s_mul = rz;
     g.s_off = r;
     if ((e = segment_states(a, c, k, g, mq, mo, true, a.dS_out, a.dz_out, a.dS_in, a.dz_in, chained, st)) != cudaSuccess) return e;
-    g.o = static_cast<__nv_bfloat16*>(a.dphk);
-    if ((e = launch<kOutE>("tc_decay_out_e", mq, mq, mo, mv, mdk, g, c, true, a.norm, chained, st)) != cudaSuccess) return e;
-    if (c.nseg == 1) {       // (the sweep that writes over dS_out when dS_in is dS_out: the last one)
-        g.last = a.dS_in;
-        g.last_z = a.dz_in;
-        g.z_state = a.dz_in != nullptr;
-    }
+    P w = g;                 // (the state that the walk leaves is dv's sweep to write)
+    w.last = w.last_z = nullptr;
+    w.o = static_cast<__nv_bfloat16*>(a.dphk);
+    if ((e = launch<kOutE>("tc_decay_out_e", mq, mq, mo, mv, mdk, w, c, true, a.norm, chained, st)) != cudaSuccess) return e;
+    g.z_state = g.last_z != nullptr;
     g.o = static_cast<__nv_bfloat16*>(a.dv);
     return out_f(mq, mk, mo, g, c, k, true, a.norm, chained, st);
 }
