@@ -58,7 +58,7 @@ __host__ __device__ constexpr int threads(int mode) { return 32 * (split(mode) ?
 // tensor memory columns.  P~ replaces the scores' first 64 columns; an output accumulator
 // takes the other 64.  T of 128 features: the first limb's 64 columns, in the modes with
 // room a second limb's, and 16 for z.
-constexpr uint32_t kColP = 0, kColOi = 64, kColOe = 128, kColDen = 192;
+constexpr uint32_t kColP = 0, kColOi = 64, kColDen = 128, kColOe = 144;   // (the scores' product is 144 wide with kColDen)
 // kOutE: two output buffers; the one-limb form puts the second one's Oi over the scores, the
 // two-limb form (128 features) has room beside them
 __host__ __device__ constexpr uint32_t col_oi(bool limbs, int b) { return limbs ? 128 + 128 * b : b ? 64 : 128; }
@@ -73,21 +73,24 @@ enum {
     B_TF = 23, B_OF = 25, B_OE = 27, B_FQE = 29, B_NUM = 33
 };
 
+// An F-side slice in the ring; in kOutF, behind its 128 rows, 16 of the z column's limbs (three
+// used): the scores' product carries the denominator's state part along.
+__host__ __device__ constexpr uint32_t slot(int mode) { return kTile + (mode == kOutF ? kExt : 0); }
+
 struct Layout {
-    uint32_t fs, fq, es, eq, y, m, zext, wext, stg, pw, smul, soff, dsum, zf, bar, tmem, total;
+    uint32_t fs, fq, es, eq, y, m, wext, stg, pw, smul, soff, dsum, zf, bar, tmem, total;
 };
 
 __host__ __device__ constexpr Layout layout(int mode)
 {
     Layout l{};
     uint32_t o = 0;
-    l.fs = o; o += 4 * kTile;                           // ring of four F-side slices
+    l.fs = o; o += 4 * slot(mode);                      // ring of four F-side slices
     l.fq = o; o += mode == kOutF ? 3 * kTile : 0;       // ring of query slices: four, or three and
     l.y = o; o += limb_tiles(mode) * kTile;             // the third of the weighted rows' limbs in that tile
     l.es = o; o += (mode == kOutF ? 1 : 2) * kTile;     // 64-wide side, two chunks (kOutF: one)
     l.eq = o; o += mode == kOutE ? 2 * kTile : 0;       // 64-wide queries, two chunks
     l.m = o; o += mode == kState ? 0 : 4 * kSlab;       // the state as an operand
-    l.zext = o; o += mode == kOutF ? 4 * kExt : 0;      // its z column, three limbs of 16 columns
     l.wext = o; o += (mode == kState ? 4 : 2) * kExt;   // z weights of the chunk's tokens, likewise
     l.stg = o; o += mode == kOutE ? 8 * 32 * 64 : 0;    // outputs on their way to the TMA store, 2 KiB a warp
     l.pw = o; o += 128 * 4;                             // lambda^d
@@ -196,6 +199,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     // features a CTA (one limb: 3.1e-3 off in relative L2, two: 1.7e-3, bf16's own rounding).
     constexpr bool kLimb = kRows;
     constexpr Layout Lo = layout(kMode);
+    constexpr uint32_t kSlot = slot(kMode);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Lo.bar);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Lo.tmem);
     const uint32_t sbase = smem_u32(sm);
@@ -228,7 +232,10 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
-    for (uint32_t i = Lo.zext / 4 + tid; i < Lo.stg / 4; i += kThreads) reinterpret_cast<uint32_t*>(sm)[i] = 0u;
+    for (uint32_t i = Lo.wext / 4 + tid; i < Lo.stg / 4; i += kThreads) reinterpret_cast<uint32_t*>(sm)[i] = 0u;
+    if (kDen)
+        for (int i = tid; i < kExt; i += kThreads)
+            reinterpret_cast<uint32_t*>(sm + Lo.fs + (i >> 9) * kSlot + kTile)[i & 511] = 0u;
     // lambda powers: within a diagonal block of scores, at 31 + distance (zero where it is masked),
     // then the column factors of a block inside the mask
     if (tid < 64) reinterpret_cast<float*>(sm + Lo.pw)[tid] = tid >= 31 && tid < 63 ? decay_pow(g2, tid - 31) : 0.0f;
@@ -277,7 +284,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                     if (u >= 4) wait_k(B_FSE + sl, (u >> 2) - 1);
                     if (s < ns) {
                         mbar_arrive_expect_tx(&bar[B_FSF + sl], kTile);
-                        tma_load_3d(sm + Lo.fs + sl * kTile, &tfs, &bar[B_FSF + sl], f0 + 64 * s, t0, bh);
+                        tma_load_3d(sm + Lo.fs + sl * kSlot, &tfs, &bar[B_FSF + sl], f0 + 64 * s, t0, bh);
                     } else {
                         mbar_arrive(&bar[B_FSF + sl]);   // the second half of the last pair: not read
                     }
@@ -305,12 +312,13 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
             constexpr uint32_t idMM = idesc_bf16(128, 64, 1, 1);
             constexpr uint32_t idMM2 = idesc_bf16(128, 128, 1, 1);
             constexpr uint32_t idMz = idesc_bf16(128, 16, 1, 0);
-            constexpr uint32_t idKz = idesc_bf16(128, 16, 0, 0);
-            constexpr uint32_t kTd = kTile >> 4, kSd = kSlab >> 4, kEd = kExt >> 4;
+            constexpr uint32_t idPz = idesc_bf16(128, 144, 0, 0);
+            constexpr uint32_t kLd = kSlot >> 4, kTd = kTile >> 4, kSd = kSlab >> 4, kEd = kExt >> 4;
             const uint64_t d0 = sdesc(sbase, 16, 1024, kLayoutSW128);
-            const uint64_t dT = sdesc(sbase, kTile, 1024, kLayoutSW128);   // the next 64 rows or columns one tile on
+            const uint64_t dT = sdesc(sbase, kTile, 1024, kLayoutSW128);   // the next 64 rows or columns one tile on,
+            const uint64_t dF = sdesc(sbase, kSlot, 1024, kLayoutSW128);   // or one ring slot on
             constexpr uint32_t oFs = Lo.fs >> 4, oFq = Lo.fq >> 4, oEs = Lo.es >> 4, oEq = Lo.eq >> 4, oY = kY >> 4,
-                               oM = Lo.m >> 4, oZe = Lo.zext >> 4, oWe = Lo.wext >> 4;
+                               oM = Lo.m >> 4, oWe = Lo.wext >> 4;
             auto wait_m = [&](int b, int k) {
                 wait_k(b, k);
                 tc_fence_after();
@@ -329,11 +337,11 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 auto slice = [&](int s) {   // F-side slice s of the chunk, complete and clean
                     const int u = i * nsE + s, sl = u & 3;
                     wait_m(B_FSF + sl, u >> 2);
-                    if (clear) clear_rows(Lo.fs + sl * kTile);
+                    if (clear) clear_rows(Lo.fs + sl * kSlot);
                     return sl;
                 };
                 auto state_pair = [&](int s) {   // T of the pair of slices s, s + 1
-                    const uint64_t da = dT + oFs + ((i * nsE + s) & 3) * kTd;
+                    const uint64_t da = dF + oFs + ((i * nsE + s) & 3) * kLd;
                     const uint32_t t = tmem + col_t(kMode, kLimb) + t_stride(kMode) * (s >> 1);
                     const uint32_t oy = oY + (kMode == kState ? eb * 3 * kTd : 0);
                     int l = 0;
@@ -362,27 +370,23 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 if (kMode == kOutF) {
                     // the scores and the state's part take the place of the last chunk's outputs
                     if (i >= 1) wait_m(B_OE, i - 1);
+                    if (kDen) wait_m(B_MF, i);   // z is behind the slices
                     for (int s = 0; s < ns; ++s) {
                         const int sl = slice(s);
                         wait_m(B_FQF + fq, fqr);
-                        const uint64_t dx = d0 + oFq + fq * kTd, dyy = d0 + oFs + sl * kTd;
+                        const uint64_t dx = d0 + oFq + fq * kTd, dyy = d0 + oFs + sl * kLd;
                         if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16(tmem + kColP, dx + 2 * kk, dyy + 2 * kk, idP, (s > 0 || kk > 0) ? 1u : 0u);
+                                umma_bf16(tmem + kColP, dx + 2 * kk, dyy + 2 * kk, kDen ? idPz : idP, (s > 0 || kk > 0) ? 1u : 0u);
                             if (s == ns - 1) umma_commit(&bar[B_PF]);
                         }
-                        if (s == 0) wait_m(B_MF, i);
+                        if (!kDen && s == 0) wait_m(B_MF, i);
                         if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 umma_bf16(tmem + kColOe, dx + 2 * kk, d0 + oM + s * kSd + 128 * kk, idKM,
                                           (s > 0 || kk > 0) ? 1u : 0u);
-                            if (kDen)
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    umma_bf16(tmem + kColDen, dx + 2 * kk, d0 + oZe + s * kEd + 2 * kk, idKz,
-                                              (s > 0 || kk > 0) ? 1u : 0u);
                             umma_commit(&bar[B_FQE + fq]);
                         }
                         if (++fq == nfq) {
@@ -430,7 +434,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                         const int v = i * ns + r, ob = v & 1;
                         if (v >= 2) wait_m(B_OE + ob, (v >> 1) - 1);
                         const uint32_t oi = tmem + col_oi(kLimb, ob), oe = tmem + col_oe(kLimb, ob);
-                        const uint64_t du = d0 + oFs + ((i * nsE + r) & 3) * kTd;
+                        const uint64_t du = d0 + oFs + ((i * nsE + r) & 3) * kLd;
                         if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
@@ -733,13 +737,13 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                             st_shared_v4(slab + 2 * kSlab + sw128_off(f & 63, 4 * half + c), l[0], l[1], l[2], l[3]);
                         }
                     if (has_zrow(b)) {
-                        if (kMode == kOutF) {
+                        if (kDen) {
                             uint16_t l[3];
                             limbs3(zrun[b], l);
-                            const uint32_t t = sbase + Lo.zext + (f >> 6) * kExt;
+                            const uint32_t t = sbase + Lo.fs + ((i * nsE + (f >> 6)) & 3) * kSlot + kTile;
 #pragma unroll
                             for (int k = 0; k < 3; ++k) st_shared_u16(t + sw128_off(k, (f & 63) >> 3) + (f & 7) * 2, l[k]);
-                        } else {
+                        } else if (kMode == kOutE) {
                             zf[(i & 1) * kMaxFw + f] = zrun[b];
                         }
                     }
