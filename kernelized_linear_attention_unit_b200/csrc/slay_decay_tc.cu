@@ -57,16 +57,16 @@ __host__ __device__ constexpr int threads(int mode) { return 32 * (split(mode) ?
 
 // tensor memory columns.  P~ replaces the scores' first 64 columns; an output accumulator
 // takes the other 64.  T of 128 features: the first limb's 64 columns, in the modes with
-// room a second limb's, and 16 for z.
+// room a second limb's (kState: a third's), and 16 for z.
 constexpr uint32_t kColP = 0, kColOi = 64, kColDen = 128, kColOe = 144;   // (the scores' product is 144 wide with kColDen)
 // kOutE: two output buffers; the one-limb form puts the second one's Oi over the scores, the
 // two-limb form (128 features) has room beside them
 __host__ __device__ constexpr uint32_t col_oi(bool limbs, int b) { return limbs ? 128 + 128 * b : b ? 64 : 128; }
 __host__ __device__ constexpr uint32_t col_oe(bool limbs, int b) { return limbs ? 192 + 128 * b : b ? 256 : 192; }
-__host__ __device__ constexpr uint32_t col_t(int mode, bool limbs) { return limbs ? 384 : mode == kOutE ? 352 : 208; }
-__host__ __device__ constexpr uint32_t col_z(int mode) { return mode == kOutE ? 64 : 128; }
-__host__ __device__ constexpr uint32_t t_stride(int mode) { return mode == kOutE ? 80 : 144; }
-__host__ __device__ constexpr int limb_tiles(int mode) { return mode == kState ? 6 : mode == kOutE ? 2 : 3; }
+__host__ __device__ constexpr uint32_t col_t(int mode, bool limbs) { return limbs ? 384 : mode == kOutE ? 352 : mode == kOutF ? 208 : 0; }
+__host__ __device__ constexpr uint32_t col_z(int mode) { return mode == kOutE ? 64 : mode == kOutF ? 128 : 192; }
+__host__ __device__ constexpr uint32_t t_stride(int mode) { return mode == kOutE ? 80 : mode == kOutF ? 144 : 208; }
+__host__ __device__ constexpr int limb_tiles(int mode) { return mode == kState ? 8 : mode == kOutE ? 2 : 3; }
 
 enum {
     B_FSF = 0, B_FSE = 4, B_FQF = 8, B_ESF = 12, B_ESE = 14, B_YF = 16, B_MF = 18, B_PF = 20, B_PT, B_OD,
@@ -91,11 +91,11 @@ __host__ __device__ constexpr Layout layout(int mode)
     l.es = o; o += (mode == kOutF ? 1 : 2) * kTile;     // 64-wide side, two chunks (kOutF: one)
     l.eq = o; o += mode == kOutE ? 2 * kTile : 0;       // 64-wide queries, two chunks
     l.m = o; o += mode == kState ? 0 : 4 * kSlab;       // the state as an operand
-    l.wext = o; o += (mode == kState ? 4 : 2) * kExt;   // z weights of the chunk's tokens, likewise
+    l.wext = o; o += mode == kState ? 0 : 2 * kExt;     // z weights of the chunk's tokens (kState: a fourth tile)
     l.stg = o; o += mode == kOutE ? 8 * 32 * 64 : 0;    // outputs on their way to the TMA store, 2 KiB a warp
     l.pw = o; o += 128 * 4;                             // lambda^d
-    l.smul = o; o += 2 * 128 * 4;                       // score scalars of the state tokens
-    l.soff = o; o += 2 * 128 * 4;
+    l.smul = o; o += mode == kState ? 0 : 2 * 128 * 4;  // score scalars of the state tokens
+    l.soff = o; o += mode == kState ? 0 : 2 * 128 * 4;
     l.dsum = o; o += mode == kOutF ? 2 * 2 * 128 * 4 : 0;   // row sums of the scores, by column half
     l.zf = o; o += mode == kOutE ? 2 * kMaxFw * 4 : 0;  // z in fp32, two chunks
     l.bar = o; o += B_NUM * 8;
@@ -223,7 +223,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     // limbs of the weighted rows: three where the fp32 state leaves the call, two (2^-17) where
     // only its bf16 copy is read; without decay and row scalars the weights are 1, one is exact
     const bool has_z = kNorm && (kMode != kOutF || !kRev || p.z_state);
-    const int nl = g2 == 0.0f && !kCols ? 1 : (kMode == kState || (kMode == kOutF && leaves)) ? 3 : 2;
+    const int nl = kMode == kState ? 3 : g2 == 0.0f && !kCols ? 1 : kMode == kOutF && leaves ? 3 : 2;
 
     // kOutF: limb tiles 0, 1 at y + 16 KiB, 2 at y, which is the query ring's fourth slot otherwise
     const int nfq = nl == 3 ? 3 : 4;
@@ -233,6 +233,12 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
         tmem_relinquish();
     }
     for (uint32_t i = Lo.wext / 4 + tid; i < Lo.stg / 4; i += kThreads) reinterpret_cast<uint32_t*>(sm)[i] = 0u;
+    if (kMode == kState)   // the z weights' 16 columns, of which three are used
+        for (int i = tid; i < 2 * kT; i += kThreads) {
+            const uint32_t t = sbase + Lo.y + ((i >> 7) * 4 + 3) * kTile;
+            st_shared_v4(t + sw128_off(i & 127, 0), 0u, 0u, 0u, 0u);
+            st_shared_v4(t + sw128_off(i & 127, 1), 0u, 0u, 0u, 0u);
+        }
     if (kDen)
         for (int i = tid; i < kExt; i += kThreads)
             reinterpret_cast<uint32_t*>(sm + Lo.fs + (i >> 9) * kSlot + kTile)[i & 511] = 0u;
@@ -343,7 +349,13 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 auto state_pair = [&](int s) {   // T of the pair of slices s, s + 1
                     const uint64_t da = dF + oFs + ((i * nsE + s) & 3) * kLd;
                     const uint32_t t = tmem + col_t(kMode, kLimb) + t_stride(kMode) * (s >> 1);
-                    const uint32_t oy = oY + (kMode == kState ? eb * 3 * kTd : 0);
+                    const uint32_t oy = oY + (kMode == kState ? eb * 4 * kTd : 0);
+                    if (kMode == kState) {   // three limbs and the z weights side by side
+                        constexpr uint32_t id = idesc_bf16(128, kNorm ? 208 : 192, 1, 1);
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) umma_bf16(t, da + 128 * kk, dT + oy + 128 * kk, id, kk > 0 ? 1u : 0u);
+                        return;
+                    }
                     int l = 0;
                     if (kMode != kOutE && nl > 1) {   // two limbs side by side: the F side is read once
 #pragma unroll
@@ -355,7 +367,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                         for (int kk = 0; kk < 8; ++kk)
                             umma_bf16(t, da + 128 * kk, d0 + (kMode == kOutF && l == 2 ? Lo.y >> 4 : oy + l * kTd) + 128 * kk, idMM, (l > 0 || kk > 0) ? 1u : 0u);
                     if (has_z) {
-                        const uint64_t dw = d0 + oWe + (kMode == kState ? eb * 2 * kEd : 0);
+                        const uint64_t dw = d0 + oWe;
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
                             umma_bf16(t + col_z(kMode), da + 128 * kk, dw + (kk >> 2) * kEd + 2 * (kk & 3), idMz, kk > 0 ? 1u : 0u);
@@ -762,7 +774,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
             const float off = kCols && in ? p.s_off[grow] : 0.0f;
             const float w = in ? decay_pow(g2, kRev ? row + 1 : n - 1 - row) : 0.0f;
             const float a = w * mul;
-            const uint32_t ybase = sbase + kY + (kMode == kState ? eb * 3 * kTile : 0);
+            const uint32_t ybase = sbase + kY + (kMode == kState ? eb * 4 * kTile : 0);
             wait_k(B_ESF + eb, i / kEs);
             uint4 r[kW / 8];
 #pragma unroll
@@ -799,11 +811,16 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 if (has_z) {
                     uint16_t l[3];
                     limbs3(kCols ? -a * off : w, l);
-                    const uint32_t t = sbase + Lo.wext + (kMode == kState ? eb * 2 * kExt : 0) + (row >> 6) * kExt;
+                    if (kMode == kState) {
+                        const uint32_t lo = l[0] | (static_cast<uint32_t>(l[1]) << 16);
+                        st_shared_v4(ybase + 3 * kTile + sw128_off(row, 0), lo, l[2], 0u, 0u);
+                    } else {
+                        const uint32_t t = sbase + Lo.wext + (row >> 6) * kExt;
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) st_shared_u16(t + sw128_off(k, (row & 63) >> 3) + (row & 7) * 2, l[k]);
+                        for (int k = 0; k < 3; ++k) st_shared_u16(t + sw128_off(k, (row & 63) >> 3) + (row & 7) * 2, l[k]);
+                    }
                 }
-                if (kCols) {
+                if (kCols && kMode != kState) {   // (kState masks no scores and has no room for them)
                     smul[(i & 1) * kT + row] = mul;
                     soff[(i & 1) * kT + row] = off;
                 }
@@ -830,9 +847,10 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 const uint32_t tc = trow + col_t(kMode, kLimb) + t_stride(kMode) * b;
 #pragma unroll
                 for (int hh = 0; hh < kW / 32; ++hh) {
-                uint32_t t[32], t2[32], z0 = 0, z1 = 0, z2 = 0;
+                uint32_t t[32], t2[32], t3[32], z0 = 0, z1 = 0, z2 = 0;
                 tmem_ld32(tc + 32 * (half + hh), t);
                 if (two) tmem_ld32(tc + 64 + 32 * half, t2);
+                if (kMode == kState) tmem_ld32(tc + 128 + 32 * half, t3);
                 if (hh == 0 && has_zrow(b)) {
                     tmem_ld1(tc + col_z(kMode), z0);
                     tmem_ld1(tc + col_z(kMode) + 1, z1);
@@ -841,13 +859,19 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 tmem_wait_ld();
                 reg_fence(t);
                 reg_fence(t2);
+                reg_fence(t3);
                 reg_fence1(z0);
                 reg_fence1(z1);
                 reg_fence1(z2);
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
                     float2 w = make_float2(__uint_as_float(t[c]), __uint_as_float(t[c + 1]));
-                    if (two) w = fadd2(w, make_float2(__uint_as_float(t2[c]), __uint_as_float(t2[c + 1])));
+                    if (kMode == kState) {   // the small limbs first
+                        const float2 w3 = make_float2(__uint_as_float(t3[c]), __uint_as_float(t3[c + 1]));
+                        w = fadd2(w, fadd2(w3, make_float2(__uint_as_float(t2[c]), __uint_as_float(t2[c + 1]))));
+                    } else if (two) {
+                        w = fadd2(w, make_float2(__uint_as_float(t2[c]), __uint_as_float(t2[c + 1])));
+                    }
                     const float2 r = ffma2(make_float2(lam, lam), make_float2(run[b][32 * hh + c], run[b][32 * hh + c + 1]), w);
                     run[b][32 * hh + c] = r.x;
                     run[b][32 * hh + c + 1] = r.y;
@@ -1105,7 +1129,7 @@ Plan plan_q(const DecayArgs& a)
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Carve {
-    float *st, *sz, *part, *part_den, *rz, *r;
+    float *st, *sz, *in, *in_z, *part, *part_den, *rz, *r;
     size_t bytes;
 };
 
@@ -1125,6 +1149,8 @@ Carve carve(const DecayArgs& a, bool bwd, void* ws)
     if (nseg > 1) {
         k.st = take(static_cast<size_t>(c.BH) * nseg * sums_floats(a.F));
         k.sz = take(static_cast<size_t>(c.BH) * nseg * a.F);
+        k.in = take(static_cast<size_t>(c.BH) * a.F * 64);
+        k.in_z = take(static_cast<size_t>(c.BH) * a.F);
     }
     if (c.nfb > 1) {
         const size_t padded = static_cast<size_t>(c.BH) * ((a.L + kT - 1) / kT) * kT;
@@ -1182,8 +1208,7 @@ P base(const DecayArgs& a, const Plan& c, int* err)
 
 // What the output sweeps start from, and the state that the walk leaves.  Up to kMaxSums
 // segments, each sweep adds up the sums of the segments before its own (66 KB each from L2, at
-// F = 256) and the one that walks last writes the state; beyond, and where that state replaces
-// the one that the other CTAs still read, a scan kernel does both.  B200, forward at F = 256:
+// F = 256) and the one that walks last writes the state; beyond, a scan kernel does both.  B200, forward at F = 256:
 // four segments (B4 H8 L2048) 44 us against 47 with the scan, nine (B1 H16 L16384) 137 against
 // 127.
 constexpr int kMaxSums = 4;
@@ -1196,7 +1221,17 @@ cudaError_t segment_states(const DecayArgs& a, const Plan& c, const Carve& k, P&
     p.last = last;
     p.last_z = last_z;
     if (c.nseg == 1) return cudaSuccess;
-    const bool scan = c.nseg > kMaxSums || (last && (last == first || (last_z && last_z == first_z)));
+    const bool scan = c.nseg > kMaxSums;
+    if (!scan && first && (last == first || (last_z && last_z == first_z))) {
+        // in place: the CTAs read a copy, one of them writes the state while others start
+        const size_t n = static_cast<size_t>(c.BH) * a.F * sizeof(float);
+        cudaError_t e = cudaMemcpyAsync(k.in, first, n * 64, cudaMemcpyDeviceToDevice, st);
+        if (e == cudaSuccess && first_z) e = cudaMemcpyAsync(k.in_z, first_z, n, cudaMemcpyDeviceToDevice, st);
+        if (e != cudaSuccess) return e;
+        p.first = k.in;
+        p.first_z = first_z ? k.in_z : nullptr;
+        chained = false;                     // the next kernel follows a copy
+    }
     P q = p;
     const Plan cs = plan(a, kMaxFw, true);   // (the sums go by blocks of 256 whatever the sweep's)
     q.nfb = cs.nfb;

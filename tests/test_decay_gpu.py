@@ -122,6 +122,11 @@ SHAPES = [  # B, H, L, F, dtype, normalize, ragged, state
     (1, 2, 2000, 512, "bf16", True, False, True),
     (1, 1, 1500, 256, "f32", False, False, True),
     (160, 1, 140, 64, "bf16", True, False, True),
+    # segments of several chunks (the sequences cut in three, four and eight)
+    (40, 1, 1100, 256, "bf16", True, False, True),
+    (37, 1, 1000, 128, "bf16", False, True, True),
+    (4, 9, 900, 320, "bf16", True, True, True),
+    (2, 9, 3000, 64, "bf16", True, False, True),
 ]
 
 
