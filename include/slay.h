@@ -30,7 +30,8 @@
  *     asynchronous on it: a returned SLAY_OK means the work was enqueued.
  *   - dtype SLAY_F32: inputs/outputs fp32, all arithmetic fp32 on CUDA cores.
  *     dtype SLAY_BF16: q,k,v,out (and dout) bf16; arithmetic with fp32 accumulation,
- *     states S and z always fp32; gradients fp32.
+ *     states S and z always fp32; gradients fp32 (slay_decay_attn_bwd: in dtype, as the
+ *     features they belong to; gradients of its states fp32).
  *   - Supported: D == Dv == 64, 1 <= R <= 16, 1 <= m, F = R*m <= 1024, eps > 0 and
  *     finite.  The bf16 tensor-core kernels take F % 128 == 0 and F <= 512 (the attention
  *     forward as feature chunks of at most 256 when F > 256), with m % 64 == 0 for the
@@ -361,7 +362,14 @@ slay_status slay_linear_attn_fwd(const void* phq, const void* phk, const void* v
  *             S_out, z_out may be S_in, z_in themselves.  A sequence of no tokens keeps its state.
  * out : device [B,H,L,Dv] in dt;  den : device [B,H,L] fp32 or NULL (without eps; NULL when
  *             normalize == 0).  eps is ignored when normalize == 0.
- * workspace : slay_workspace_bytes(SLAY_OP_DECAY_FWD, dt, B, H, L, 64, Dv, 1, F) bytes. */
+ * workspace : slay_workspace_bytes(SLAY_OP_DECAY_FWD, dt, B, H, L, 64, Dv, 1, F) bytes; it
+ *             serves one call at a time.
+ * Outputs share no memory with inputs, but for the states.  A token of a sequence that is not
+ * finite may reach every row of its 128-token chunk.  B*H <= 21845.
+ * bf16 with F % 8 == 0, F <= 512 runs on tensor cores (SLAY_PATH_TC_CONTRACTION): fp32
+ * accumulation; the masked scores and the state's operand are rounded to bf16, den and the
+ * states are not (token weights enter the states as three bf16 limbs).  fp32, and other F, run
+ * on CUDA cores in fp32. */
 slay_status slay_decay_attn_fwd(const void* phq, const void* phk, const void* v,
                                 const float* log_decay, const int32_t* lengths,
                                 const float* S_in, const float* z_in, void* out, float* den,
@@ -379,10 +387,12 @@ slay_status slay_decay_attn_fwd(const void* phq, const void* phk, const void* v,
  * phq, phk, v, log_decay, lengths, S_in, z_in : as the forward was given them.
  * out, den   : the forward's (read when normalize != 0, else ignored); dout : [B,H,L,Dv] in dt.
  * dS_out, dz_out : gradients of the final state, fp32, NULL: zero.
- * dphq, dphk [B,H,L,F], dv [B,H,L,Dv] : written, in dt (slay_feature_map_bwd takes them); rows
- *             behind a sequence are left as they were.
+ * dphq, dphk [B,H,L,F], dv [B,H,L,Dv] : written, in dt (slay_feature_map_bwd takes dphq and
+ *             dphk in it); rows behind a sequence are left as they were.
  * dS_in, dz_in : fp32, NULL: not wanted; may be dS_out, dz_out themselves.
- * workspace  : slay_workspace_bytes(SLAY_OP_DECAY_BWD, dt, B, H, L, 64, Dv, 1, F) bytes. */
+ * workspace  : slay_workspace_bytes(SLAY_OP_DECAY_BWD, dt, B, H, L, 64, Dv, 1, F) bytes.
+ * Paths, limits and the rest as slay_decay_attn_fwd; on tensor cores the normalized dphq, a
+ * difference, takes its scores and states as two bf16 limbs. */
 slay_status slay_decay_attn_bwd(const void* phq, const void* phk, const void* v,
                                 const float* log_decay, const int32_t* lengths,
                                 const float* S_in, const float* z_in, const void* out,

@@ -649,9 +649,11 @@ def _decay_common(phq, phk, v, log_decay, lengths):
     return dev, B, H, L, F, v.shape[-1]
 
 
-def _decay_workspace(op, dt, B, H, L, F, Dv, workspace, dev):
+def _decay_workspace(op, dt, B, H, L, F, Dv, workspace, dev, stream):
     if workspace is None:
         workspace = alloc_workspace(op, dt, B, H, L, 64, Dv, 1, F, dev)
+        if stream is not None:   # allocated on the current stream, used on the caller's
+            workspace.record_stream(stream)
     _check_on(dev, workspace, "workspace")
     return workspace, workspace.numel() * workspace.element_size()
 
@@ -668,7 +670,7 @@ def slay_decay_attn_fwd(phq, phk, v, log_decay, out, den=None, normalize=True, e
     _decay_pair(dev, S_in, z_in, (B, H, F), normalize, "in")
     _decay_pair(dev, S_out, z_out, (B, H, F), normalize, "out")
     dt = _dt(phq)
-    workspace, wbytes = _decay_workspace(OP_DECAY_FWD, dt, B, H, L, F, Dv, workspace, dev)
+    workspace, wbytes = _decay_workspace(OP_DECAY_FWD, dt, B, H, L, F, Dv, workspace, dev, stream)
     _call_on(dev, stream, lib().slay_decay_attn_fwd, "slay_decay_attn_fwd", (
         phq.data_ptr(), phk.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(lengths), _addr(S_in),
         _addr(z_in), out.data_ptr(), _addr(den), _addr(S_out), _addr(z_out), B, H, L, F, Dv, dt,
@@ -693,7 +695,7 @@ def slay_decay_attn_bwd(phq, phk, v, log_decay, dout, dphq, dphk, dv, out=None, 
     _decay_pair(dev, dS_out, dz_out, (B, H, F), normalize, "out gradient")
     _decay_pair(dev, dS_in, dz_in, (B, H, F), normalize, "in gradient")
     dt = _dt(phq)
-    workspace, wbytes = _decay_workspace(OP_DECAY_BWD, dt, B, H, L, F, Dv, workspace, dev)
+    workspace, wbytes = _decay_workspace(OP_DECAY_BWD, dt, B, H, L, F, Dv, workspace, dev, stream)
     _call_on(dev, stream, lib().slay_decay_attn_bwd, "slay_decay_attn_bwd", (
         phq.data_ptr(), phk.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(lengths), _addr(S_in),
         _addr(z_in), _addr(out), _addr(den), dout.data_ptr(), _addr(dS_out), _addr(dz_out),

@@ -11,18 +11,25 @@
 // Oi and Oe stay apart so that the row factor lambda^(i+1) is applied in fp32.
 //
 // Roundings to bf16 (all else is fp32): P~ and the copy of M that the tensor core reads, one
-// each, so an output sees two besides its own; the decay weight of a token's state term is
-// folded into the 64-wide side as w_j u_j = hi + mid + lo, three bf16 limbs accumulated in the
-// same accumulator, so the fp32 states that leave the call are as exact as fp32 sums (one limb
-// alone would be off by 2^-9, two by 2^-17).  The z column (the ones column of u) takes its
-// weights as three bf16 columns of a 16-wide operand, exactly as well, and so does the
-// denominator's state part; the denominator's other part is summed in fp32 from the scores.
+// each, so an output sees two besides its own (the normalized dphq takes both in two limbs);
+// the decay weight of a token's state term is folded into the 64-wide side as w_j u_j = hi +
+// mid + lo, three bf16 limbs, where the fp32 state leaves the call, so that it is as exact as an
+// fp32 sum (one limb alone would be off by 2^-9), and two (2^-17) where only its bf16 copy is
+// read.  The z column (the ones column of u) takes its weights as three bf16 columns of a
+// 16-wide operand, and so does the denominator's state part; the denominator's other part is
+// summed in fp32 from the scores.
 //
-// Bound: HBM.  A 128-token chunk at F = 256 moves 164 KB (7000 clocks at an SM's share of the
-// bandwidth) and needs about 1800 clocks of tensor-core time, three state limbs included.  When
-// there are fewer (b, h) than SMs the sequence is cut into segments: k_tc_dec<kState> sums each
-// segment's own state (reading the F side and the 64-wide side once more), k_dec_seg_scan
-// turns those into the states entering each segment, and the output sweeps start from them.
+// Bounds.  HBM's floor is 2 (2 F + 128) bytes per token and head forward, 2 (4 F + 256)
+// backward; a 128-token chunk at F = 256 is 164 KB, 7000 clocks at an SM's share of the
+// bandwidth.  The MMAs read their operands from shared memory (M = 128, K = 16: 4 KB of A and
+// 2 KB of B per 64 columns, 128 bytes a clock), 4000 of them for the 88 MMAs of a forward
+// chunk, which is why accumulators are as wide as tensor memory allows; P~ is read from tensor
+// memory.  The chain of a chunk (scores, masking, state sum, its bf16 copy, the next scores)
+// takes 8000 to 9000 clocks: forward B32 H12 L1024 F256 in 104 us, 4.9 TB/s, 74% of the copy
+// bandwidth; with fewer (b, h) than SMs the sequence is cut into segments, whose sums
+// (k_tc_dec<kState>) read the F side once more.  Measured alternatives: 512 threads with four
+// state warps in kOutF, too, 121 against 104 us; MMA loops not unrolled 126 us; roles chosen at
+// run time 162 us (the code outgrew the instruction cache).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

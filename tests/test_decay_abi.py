@@ -101,6 +101,16 @@ def test_workspace_sizes():
     assert _bwd(ws_bytes=need - 256) == BAD
 
 
+@pytest.mark.parametrize("dt,F,want", [("BF16", 256, 2), ("BF16", 8, 2), ("BF16", 512, 2), ("BF16", 520, 0), ("BF16", 100, 0),
+                                       ("F32", 256, 0)])
+def test_path(dt, F, want):
+    for op in (bd.OP_DECAY_FWD, bd.OP_DECAY_BWD):
+        assert bd.slay_path(op, getattr(bd, "SLAY_" + dt), 1, 2, 100, 64, 64, 1, F) == want
+        assert bd.slay_path(op, getattr(bd, "SLAY_" + dt), 0, 2, 100, 64, 64, 1, F) == 0
+    with pytest.raises(bd.SlayError):
+        bd.slay_path(bd.OP_DECAY_FWD, bd.SLAY_BF16, 1, 2, 100, 64, 32, 1, F)
+
+
 def test_binding_checks():
     import torch
     x = torch.zeros(1, 1, 4, 8)

@@ -101,6 +101,9 @@ def _valid_only(x, lengths):
 SHAPES = [  # B, H, L, F, dtype, normalize, ragged, state
     (1, 1, 1, 64, "bf16", True, False, False),
     (1, 2, 1, 40, "f32", True, False, True),
+    (3, 2, 70, 8, "bf16", True, True, True),
+    (1, 1, 129, 1, "bf16", False, False, True),
+    (1, 2, 90, 1024, "bf16", True, False, True),
     (2, 3, 2, 128, "bf16", False, False, True),
     (2, 6, 63, 64, "bf16", True, False, True),
     (1, 6, 64, 33, "f32", True, False, True),
@@ -223,6 +226,46 @@ def test_no_decay_is_the_plain_contraction():
     o2, d2 = torch.empty_like(out), torch.empty_like(den)
     bd.slay_linear_attn_fwd(c["phq"], c["phk"], c["v"], o2, d2, c["eps"], True)
     assert float((out - o2).norm() / o2.norm()) <= 1e-5 and float((den - d2).norm() / d2.norm()) <= 1e-5
+
+
+def test_optional_outputs_change_nothing():
+    c, _ = _case(3, 2, 700, 256, "bf16", True, True, True, kind="slow")
+    a = _forward(c, "bf16")[0]
+    b = _forward(c, "bf16", den=False, state_out=False)[0]
+    # (the state that leaves is summed from three limbs, the one inside from two: 2^-17)
+    assert float((a - b).float().norm() / a.float().norm()) <= 2.0 ** -9
+
+
+def test_larger_workspace_and_reuse():
+    """One workspace, larger than any of the calls needs, for calls of several sizes in a row."""
+    ws = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    for shape in ((1, 4, 900, 128), (2, 3, 257, 512), (40, 1, 300, 64), (1, 1, 5000, 256)):
+        c, _ = _case(*shape, "bf16", True, False, False, kind="slow")
+        want = _forward(c, "bf16")[0]
+        out = torch.empty_like(want)
+        assert bd.slay_decay_attn_fwd(out=out, workspace=ws, **c) is ws
+        bd.slay_kernel_status(ws)
+        assert float((out - want).float().norm() / want.float().norm()) <= 2.0 ** -9
+
+
+def test_path_is_what_runs():
+    for dt, F, tc in (("bf16", 256, True), ("bf16", 8, True), ("bf16", 512, True), ("bf16", 520, False), ("bf16", 36, False),
+                      ("f32", 256, False)):
+        c, g = _case(1, 2, 300, F, dt, True, False, False)
+        bd.slay_trace_enable(True)
+        try:
+            bd.slay_trace_read()
+            out, den, _, _ = _forward(c, dt)
+            fwd = [n for n, _ in bd.slay_trace_read()]
+            grads = [torch.empty_like(c[k]) for k in ("phq", "phk", "v")]
+            bd.slay_decay_attn_bwd(c["phq"], c["phk"], c["v"], c["log_decay"], torch.ones_like(out), *grads, out=out, den=den)
+            torch.cuda.synchronize()
+            bwd = [n for n, _ in bd.slay_trace_read()]
+        finally:
+            bd.slay_trace_enable(False)
+        for op, names in ((bd.OP_DECAY_FWD, fwd), (bd.OP_DECAY_BWD, bwd)):
+            assert any(n.startswith("tc_decay") for n in names) == tc, names
+            assert bd.slay_path(op, TDT[dt], 1, 2, 300, 64, 64, 1, F) == (bd.PATH_TC_CONTRACTION if tc else 0)
 
 
 @pytest.mark.parametrize("L", [0, 1, 300, 2500])
