@@ -278,7 +278,8 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
 
     // Registers: the loading warpgroup gives some of its share to the warps that hold the
     // state.  384 threads launch with 168 each: 88 + 2 x 208 = 3 x 168; 512 with 128:
-    // 64 + 192 + 2 x 128 = 4 x 128.
+    // 64 + 192 + 2 x 128 = 4 x 128, or, with half the state and two limbs of scores,
+    // 64 + 128 + 2 x 160.
     if (warp < 4) {
         regs_dec<kSplit ? 64 : 88>();
         if (warp == 1 && lane == 0) {
@@ -690,16 +691,18 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
             }
         };
         if (kSplit && warp >= 8) {
+            if (kLimb) regs_inc<160>();
             for (int i = 0; i < count; ++i) out_e(i);
             if (lane == 0) bulk_wait<0>();   // this warp's stores have landed
         } else {
-        regs_inc<kSplit ? 192 : 208>();
-        float run[2][kW], zrun[2] = {0.0f, 0.0f};   // M at (f = 128 b + row, e = 32 half + c); z at b
+        if (!kLimb) regs_inc<kSplit ? 192 : 208>();
+        constexpr int kNb = kLimb ? 1 : 2;      // 128-feature blocks
+        float run[kNb][kW], zrun[kNb] = {};   // M at (f = 128 b + row, e = 32 half + c); z at b
         auto has_zrow = [&](int b) { return has_z && (kSplit || b == half); };
         // the state entering the segment: M <- lambda^n M + (its sums) over the segments before it
         auto add_state = [&](const float* S, const float* z, int64_t at, float lam, bool own) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < kNb; ++b) {
                 const int f = 128 * b + row;
                 if (f >= fv) continue;
                 const float4* src = own ? reinterpret_cast<const float4*>(S + at * sums_floats(p.F)) + sums_at(f0 + f, 8 * half)
@@ -717,7 +720,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
             }
         };
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < kNb; ++b)
 #pragma unroll
             for (int c = 0; c < kW; ++c) run[b][c] = 0.0f;
         if (p.starts) {
@@ -734,7 +737,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
         // the operand copy of M, and its z column, for chunk i
         auto write_m = [&](int i) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < kNb; ++b) {
                 const int f = 128 * b + row;
                 if (f < 64 * ns) {
                     const uint32_t slab = sbase + Lo.m + (f >> 6) * kSlab;
@@ -845,7 +848,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 tc_fence_after();
             }
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < kNb; ++b) {
                 if (2 * b >= ns) break;
                 if (kMode == kState) {
                     wait_k(B_TF + b, i);
@@ -1011,7 +1014,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
         if (leaves) {
             const int64_t at = kMode == kState ? sidx : bh;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < kNb; ++b) {
                 const int f = 128 * b + row;
                 if (f >= fv) continue;
                 float4* dst = kMode == kState ? reinterpret_cast<float4*>(p.last + at * sums_floats(p.F)) + sums_at(f0 + f, 8 * half)
