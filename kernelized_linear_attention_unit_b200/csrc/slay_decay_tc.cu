@@ -278,10 +278,11 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
 
     // Registers: the loading warpgroup gives some of its share to the warps that hold the
     // state.  384 threads launch with 168 each: 88 + 2 x 208 = 3 x 168; 512 with 128:
-    // 64 + 192 + 2 x 128 = 4 x 128, or, with half the state and two limbs of scores,
+    // 96 + 192 + 2 x 112 = 4 x 128 (64 + 192 + 2 x 128 spilled in the loading warps: dphk of
+    // B2 H16 L8192 F512 174 against 162 us), or, with half the state and two limbs of scores,
     // 64 + 128 + 2 x 160.
     if (warp < 4) {
-        regs_dec<kSplit ? 64 : 88>();
+        regs_dec<kLimb ? 64 : kSplit ? 96 : 88>();
         if (warp == 1 && lane == 0) {
             // -------------------------------------------------------------- TMA loads
             for (int i = 0; i < count && wt.ok; ++i) {
@@ -692,6 +693,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
         };
         if (kSplit && warp >= 8) {
             if (kLimb) regs_inc<160>();
+            else regs_dec<112>();
             for (int i = 0; i < count; ++i) out_e(i);
             if (lane == 0) bulk_wait<0>();   // this warp's stores have landed
         } else {
