@@ -616,15 +616,17 @@ def _addr(t):
 
 def _call_on(device, stream, fn, name, args):
     """fn(*args, stream) with `device` current; stream: the caller's, or that device's current one."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
+    if stream is None:   # current_stream(device).cuda_stream without the object (2 us of a small call)
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
     elif stream.device != device:
         raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+    else:
+        raw = stream.cuda_stream
     if torch.cuda.current_device() == device.index:
-        status = fn(*args, stream.cuda_stream)
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, stream.cuda_stream)
+            status = fn(*args, raw)
     _raise(status, name)
 
 
