@@ -3,7 +3,9 @@
 // are described in slay_decay.h.
 //
 // Three kernels over 64-token chunks, every product a 64 x 64 block of a 256-thread CTA held
-// as 4 x 4 fp32 accumulators per thread, operands in shared memory as fp32:
+// as 4 x 4 fp32 accumulators per thread, operands in shared memory as fp32, two products an
+// instruction (B4 H16 L1024 F64 forward 106 us one by one, 100 in pairs; 81 with the loads
+// asynchronous and the first of them ahead of the wait for the kernel in front):
 //   k_dec_state : each chunk's own state  T = sum_j w_j y_j u_j^T  (a CTA per 64 features)
 //   k_dec_scan  : the states entering each chunk, M <- lambda^n M + T, one thread per element
 //   k_dec_fwd, k_dec_grads : the outputs, per chunk out_f (queries on the F side: out, dv;
@@ -75,24 +77,34 @@ __device__ __forceinline__ int seq_len(const int32_t* lengths, int b, int L)
     return lengths ? min(max(lengths[b], 0), L) : L;
 }
 
-// rows [t0, t0 + n) x columns [c0, c0 + 64) of x [.., W] -> dst [64][kPitch] fp32, times
-// mul[row] when given; everything else zero
+// `rows` rows of x [.., W], columns [c0, c0 + 64) -> dst [rows][kPitch] fp32, times mul[row]
+// when given; rows past n and columns past W are zero.  fp32 without mul arrives asynchronously:
+// loads_done() before it is read.
 template <typename T>
-__device__ __forceinline__ void load_block(float* dst, const T* x, int n, int W, int c0, const float* mul)
+__device__ __forceinline__ void load_block(float* dst, const T* x, int rows, int n, int W, int c0,
+                                           const float* mul = nullptr)
 {
+    constexpr bool kAsync = sizeof(T) == 4;
     const int wc = min(64, W - c0);
     if ((W & 3) == 0) {
-        for (int i = threadIdx.x; i < 64 * 16; i += kNT) {
+        for (int i = threadIdx.x; i < rows * 16; i += kNT) {
             const int r = i >> 4, c = (i & 15) * 4;
+            const bool in = r < n && c < wc;
+            const T* from = in ? x + static_cast<int64_t>(r) * W + c0 + c : x;
+            if (kAsync && !mul) {
+                const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst + r * kPitch + c));
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+                continue;
+            }
             float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < n && c < wc) {
-                w = ld4(x + static_cast<int64_t>(r) * W + c0 + c);
+            if (in) {
+                w = ld4(from);
                 if (mul) { const float m = mul[r]; w.x *= m; w.y *= m; w.z *= m; w.w *= m; }
             }
             *reinterpret_cast<float4*>(dst + r * kPitch + c) = w;
         }
     } else {
-        for (int i = threadIdx.x; i < 64 * 64; i += kNT) {
+        for (int i = threadIdx.x; i < rows * 64; i += kNT) {
             const int r = i >> 6, c = i & 63;
             float w = 0.0f;
             if (r < n && c < wc) {
@@ -103,52 +115,76 @@ __device__ __forceinline__ void load_block(float* dst, const T* x, int n, int W,
         }
     }
 }
+__device__ __forceinline__ void loads_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kOpen>   // but the last kOpen groups sent
+__device__ __forceinline__ void loads_done() { asm volatile("cp.async.wait_group %0;" ::"n"(kOpen) : "memory"); }
 
-// acc[a][b] += sum_k A[ty + 16 a][k] B[tx + 16 b][k], k < 64
-__device__ __forceinline__ void mma_nt(float (&acc)[4][4], const float* A, const float* B, int ty, int tx)
+// d += a b on two floats at once
+__device__ __forceinline__ void fma2(float2& d, float2 a, float2 b)
 {
-#pragma unroll 4
-    for (int k = 0; k < 64; k += 4) {
-        float4 a[4], b[4];
+    asm("fma.rn.f32x2 %0, %1, %2, %0;"
+        : "+l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+}
+
+// acc[i][..] += a[i] b[..] for a thread's R x 4 block
+template <int R>
+__device__ __forceinline__ void outer(float2 (&acc)[R][2], const float (&a)[R], float4 b)
+{
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * kPitch + k);
-            b[i] = *reinterpret_cast<const float4*>(B + (tx + 16 * i) * kPitch + k);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
-                acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
-                acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
-                acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
-            }
+    for (int i = 0; i < R; ++i) {
+        const float2 w = make_float2(a[i], a[i]);
+        fma2(acc[i][0], w, make_float2(b.x, b.y));
+        fma2(acc[i][1], w, make_float2(b.z, b.w));
     }
 }
 
-// acc[a][b] += sum_k A[ty + 16 a][k] B[k][4 tx + b], k < 64
-__device__ __forceinline__ void mma_nn(float (&acc)[4][4], const float* A, const float* B, int ty, int tx)
+// acc[a][b] += sum_k A[ty + 16 a][k] B[tx + 16 b][k], k < 64
+template <int R>
+__device__ __forceinline__ void mma_nt(float (&acc)[R][4], const float* A, const float* B, int ty, int tx)
+{
+    float2 even_odd[R][4] = {};   // sums over even and over odd k
+#pragma unroll 4
+    for (int k = 0; k < 64; k += 4) {
+        float4 a[R], b[4];
+#pragma unroll
+        for (int i = 0; i < R; ++i) a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * kPitch + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * kPitch + k);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                fma2(even_odd[i][j], make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y));
+                fma2(even_odd[i][j], make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w));
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] += even_odd[i][j].x + even_odd[i][j].y;
+}
+
+// acc[a] (columns 4 tx to 4 tx + 3) += sum_k A[ty + 16 a][k] B[k][..], k < 64
+template <int R>
+__device__ __forceinline__ void mma_nn(float2 (&acc)[R][2], const float* A, const float* B, int ty, int tx)
 {
 #pragma unroll 4
     for (int k = 0; k < 64; k += 4) {
-        float4 a[4], b[4];
+        float a[4][R];
+        float4 b[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * kPitch + k);
-            b[i] = *reinterpret_cast<const float4*>(B + (k + i) * kPitch + 4 * tx);
+        for (int i = 0; i < R; ++i) {
+            const float4 w = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * kPitch + k);
+            a[0][i] = w.x;
+            a[1][i] = w.y;
+            a[2][i] = w.z;
+            a[3][i] = w.w;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float av[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+        for (int i = 0; i < 4; ++i) b[i] = *reinterpret_cast<const float4*>(B + (k + i) * kPitch + 4 * tx);
 #pragma unroll
-            for (int k2 = 0; k2 < 4; ++k2) {
-                acc[i][0] = fmaf(av[k2], b[k2].x, acc[i][0]);
-                acc[i][1] = fmaf(av[k2], b[k2].y, acc[i][1]);
-                acc[i][2] = fmaf(av[k2], b[k2].z, acc[i][2]);
-                acc[i][3] = fmaf(av[k2], b[k2].w, acc[i][3]);
-            }
-        }
+        for (int i = 0; i < 4; ++i) outer<R>(acc, a[i], b[i]);
     }
 }
 
@@ -175,6 +211,8 @@ __global__ void __launch_bounds__(kNT) k_dec_state(Sweep s0, Sweep s1, int BH)
     const float g2 = s.log_decay[bh % s.H] * kLog2e;
     float* st = s.st + ((bh * s.nc + c) * s.F + f0) * 64;
     const int64_t row0 = bh * s.L + t0;
+    load_block(fsm, static_cast<const T*>(s.fs) + row0 * s.F, kC, n, s.F, f0);
+    loads_sent();
     after_previous_kernel();
     if (tid < kC) {
         float a = 0.0f, b = 0.0f;
@@ -188,28 +226,20 @@ __global__ void __launch_bounds__(kNT) k_dec_state(Sweep s0, Sweep s1, int BH)
         wz[tid] = b;
     }
     __syncthreads();
-    load_block(fsm, static_cast<const T*>(s.fs) + row0 * s.F, n, s.F, f0, nullptr);
-    load_block(esm, static_cast<const T*>(s.es) + row0 * 64, n, 64, 0, w);
+    load_block(esm, static_cast<const T*>(s.es) + row0 * 64, kC, n, 64, 0, w);
+    loads_done<0>();
     __syncthreads();
-    float acc[4][4] = {};
+    float2 acc[4][2] = {};
 #pragma unroll 8
     for (int j = 0; j < kC; ++j) {
         const float4 a = *reinterpret_cast<const float4*>(fsm + j * kPitch + 4 * ty);
-        const float4 b = *reinterpret_cast<const float4*>(esm + j * kPitch + 4 * tx);
-        const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            acc[i][0] = fmaf(av[i], b.x, acc[i][0]);
-            acc[i][1] = fmaf(av[i], b.y, acc[i][1]);
-            acc[i][2] = fmaf(av[i], b.z, acc[i][2]);
-            acc[i][3] = fmaf(av[i], b.w, acc[i][3]);
-        }
+        outer<4>(acc, {a.x, a.y, a.z, a.w}, *reinterpret_cast<const float4*>(esm + j * kPitch + 4 * tx));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (f0 + 4 * ty + i < s.F)
             *reinterpret_cast<float4*>(st + (4 * ty + i) * 64 + 4 * tx) =
-                make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+                make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
     if (s.sz && tid < 64 && f0 + tid < s.F) {
         float z = 0.0f;
         for (int j = 0; j < kC; ++j) z = fmaf(wz[j], fsm[j * kPitch + tid], z);
@@ -271,123 +301,158 @@ __device__ __forceinline__ float score(float raw, int i, int j, int n, bool rev,
     return d >= 0 && i < n && j < n ? (raw - qo - so) * (qm * sm_mul[j]) * pw[d] : 0.0f;
 }
 
+// The outputs' kernels take R x 16 of the chunk's queries a CTA, R rows a thread; what they
+// read of the call's own inputs (nothing in the chain writes those) is on its way before the
+// kernels in front of them have ended.
+
 // ----------------------------------------------------- outputs 64 wide (out, dv)
-template <typename T>
-__device__ __forceinline__ void out_f(const Sweep& s, float* sm, int64_t bh, T* o, float* den, bool norm, float eps)
+template <typename T, int R>
+__device__ __forceinline__ void out_f(const Sweep& s, float* sm, int64_t bh, int part, T* o, float* den, bool norm, float eps)
 {
-    float* fqs = sm;                        // [64 i][64 f]
-    float* fss = fqs + 64 * kPitch;         // [64 j][64 f]; then the scores [64 i][64 j]
-    float* ms = fss + 64 * kPitch;          // [64 f][64 e]; then the E side [64 j][64 e]
-    __shared__ float pw[kC], smul[kC], zs[64], dsum[kC];
-    const int c = blockIdx.x;
+    constexpr int kRows = 16 * R;
+    float* fqs = sm;                        // [kRows i][64 f]
+    float* fss = fqs + 64 * kPitch;         // [64 j][64 f]; then the scores [kRows i][64 j]
+    float* ms = fss + 64 * kPitch;          // [64 f][64 e]
+    float* ess = ms + 64 * kPitch;          // [64 j][64 e]
+    __shared__ float pw[kC], smul[kC], zs[64], dsum[kRows];
+    const int c = blockIdx.x, i0 = part * kRows;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int t0 = c * kC, n = min(kC, seq_len(s.lengths, static_cast<int>(bh / s.H), s.L) - t0);
-    after_previous_kernel();
-    if (n <= 0) return;
     const float g2 = s.log_decay[bh % s.H] * kLog2e;
     const int64_t row0 = bh * s.L + t0;
-    if (tid < kC) {
-        pw[tid] = decay_pow(g2, tid);
-        smul[tid] = tid < n && s.s_mul ? s.s_mul[row0 + tid] : 1.0f;
-        dsum[tid] = 0.0f;
-    }
-    float p[4][4] = {}, acc[4][4] = {}, dz = 0.0f;
-    for (int f0 = 0; f0 < s.F; f0 += 64) {
-        __syncthreads();
-        load_block(fqs, static_cast<const T*>(s.fq) + row0 * s.F, n, s.F, f0, nullptr);
-        load_block(fss, static_cast<const T*>(s.fs) + row0 * s.F, n, s.F, f0, nullptr);
-        load_block(ms, s.st + ((bh * s.nc + c) * s.F + f0) * 64, min(64, s.F - f0), 64, 0, nullptr);
+    auto load_rows = [&](int f0) {
+        load_block(fqs, static_cast<const T*>(s.fq) + (row0 + i0) * s.F, kRows, n - i0, s.F, f0);
+        load_block(fss, static_cast<const T*>(s.fs) + row0 * s.F, kC, n, s.F, f0);
+    };
+    auto load_state = [&](int f0) {
+        load_block(ms, s.st + ((bh * s.nc + c) * s.F + f0) * 64, 64, min(64, s.F - f0), 64, 0);
         if (norm && tid < 64) zs[tid] = f0 + tid < s.F ? s.sz[(bh * s.nc + c) * s.F + f0 + tid] : 0.0f;
+    };
+    if (n > i0) load_rows(0);
+    if (tid < kC) pw[tid] = decay_pow(g2, tid);
+    if (tid < kRows) dsum[tid] = 0.0f;
+    after_previous_kernel();
+    if (n <= i0) return;
+    load_state(0);
+    loads_sent();
+    load_block(ess, static_cast<const T*>(s.es) + row0 * 64, kC, n, 64, 0);
+    loads_sent();
+    if (tid < kC) smul[tid] = tid < n && s.s_mul ? s.s_mul[row0 + tid] : 1.0f;
+    float p[R][4] = {}, dz = 0.0f;
+    float2 acc[R][2] = {};
+    constexpr int kLanes = kNT / kRows, kEach = 64 / kLanes;   // threads of a row and their features of z
+    loads_done<1>();
+    for (int f0 = 0;;) {
         __syncthreads();
-        mma_nt(p, fqs, fss, ty, tx);
-        mma_nn(acc, fqs, ms, ty, tx);
-        if (norm) {   // four threads a row, 16 features each
-            const int i = tid >> 2, k0 = (tid & 3) * 16;
+        mma_nt<R>(p, fqs, fss, ty, tx);
+        mma_nn<R>(acc, fqs, ms, ty, tx);
+        if (norm) {
+            const int i = tid / kLanes, k0 = (tid % kLanes) * kEach;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) dz = fmaf(fqs[i * kPitch + k0 + k], zs[k0 + k], dz);
+            for (int k = 0; k < kEach; ++k) dz = fmaf(fqs[i * kPitch + k0 + k], zs[k0 + k], dz);
         }
+        __syncthreads();
+        f0 += 64;
+        if (f0 >= s.F) break;
+        load_rows(f0);
+        load_state(f0);
+        loads_sent();
+        loads_done<0>();
     }
-    __syncthreads();
-    float rs[4] = {};
+    float rs[R] = {};
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < R; ++a)
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const int i = ty + 16 * a, j = tx + 16 * b;
-            const float w = score(p[a][b], i, j, n, s.rev, 0.0f, 0.0f, 1.0f, smul, pw);
+            const float w = score(p[a][b], i0 + i, j, n, s.rev, 0.0f, 0.0f, 1.0f, smul, pw);
             fss[i * kPitch + j] = w;
             rs[a] += w;
         }
     if (norm) {
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
+        for (int a = 0; a < R; ++a) {
             for (int x = 8; x > 0; x >>= 1) rs[a] += __shfl_xor_sync(0xffffffffu, rs[a], x);
             if (tx == 0) dsum[ty + 16 * a] = rs[a];
         }
-        dz += __shfl_xor_sync(0xffffffffu, dz, 1);
-        dz += __shfl_xor_sync(0xffffffffu, dz, 2);
+#pragma unroll
+        for (int x = 1; x < kLanes; x *= 2) dz += __shfl_xor_sync(0xffffffffu, dz, x);
     }
-    load_block(ms, static_cast<const T*>(s.es) + row0 * 64, n, 64, 0, nullptr);
+    loads_done<0>();
     __syncthreads();
-    if (norm && (tid & 3) == 0) {
-        const int i = tid >> 2;
-        const float d = fmaf(decay_pow(g2, s.rev ? max(n - 1 - i, 0) : i + 1), dz, dsum[i]);
+    if (norm && tid % kLanes == 0) {
+        const int i = tid / kLanes;
+        const float d = fmaf(decay_pow(g2, s.rev ? max(n - 1 - i0 - i, 0) : i0 + i + 1), dz, dsum[i]);
         dsum[i] = d;
-        if (den && i < n) den[row0 + i] = d;
+        if (den && i0 + i < n) den[row0 + i0 + i] = d;
     }
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-        const int i = ty + 16 * a;
+    for (int a = 0; a < R; ++a) {
+        const int i = i0 + ty + 16 * a;
         const float fac = decay_pow(g2, s.rev ? max(n - 1 - i, 0) : i + 1);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) acc[a][b] *= fac;
+        for (int b = 0; b < 2; ++b) acc[a][b] = make_float2(acc[a][b].x * fac, acc[a][b].y * fac);
     }
-    mma_nn(acc, fss, ms, ty, tx);
+    mma_nn<R>(acc, fss, ess, ty, tx);
     if (norm) __syncthreads();
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
+    for (int a = 0; a < R; ++a) {
         const int i = ty + 16 * a;
-        if (i >= n) continue;
+        if (i0 + i >= n) continue;
         const float rden = norm ? dsum[i] + eps : 1.0f;
-        float4 w = make_float4(acc[a][0], acc[a][1], acc[a][2], acc[a][3]);
+        float4 w = make_float4(acc[a][0].x, acc[a][0].y, acc[a][1].x, acc[a][1].y);
         if (norm) { w.x /= rden; w.y /= rden; w.z /= rden; w.w /= rden; }
-        st4(o + (row0 + i) * 64 + 4 * tx, w);
+        st4(o + (row0 + i0 + i) * 64 + 4 * tx, w);
     }
 }
 
 // ----------------------------------------------------- outputs F wide (dphq, dphk)
-template <typename T>
-__device__ __forceinline__ void out_e(const Sweep& s, float* sm, int64_t bh, T* o, bool norm)
+template <typename T, int R>
+__device__ __forceinline__ void out_e(const Sweep& s, float* sm, int64_t bh, int part, int group, int groups, T* o, bool norm)
 {
-    float* eqs = sm;                        // [64 i][64 e]
-    float* ps = eqs + 64 * kPitch;          // E side of the state, then the scores [64 i][64 j]
+    constexpr int kRows = 16 * R;
+    float* eqs = sm;                        // [kRows i][64 e]
+    float* ps = eqs + 64 * kPitch;          // E side of the state, then the scores [kRows i][64 j]
     float* fss = ps + 64 * kPitch;          // [64 j][64 f]
     float* ms = fss + 64 * kPitch;          // [64 f][64 e]
     __shared__ float pw[kC], smul[kC], soff[kC], zs[64];
-    const int c = blockIdx.x;
+    const int c = blockIdx.x, i0 = part * kRows;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int t0 = c * kC, n = min(kC, seq_len(s.lengths, static_cast<int>(bh / s.H), s.L) - t0);
-    after_previous_kernel();
-    if (n <= 0) return;
     const float g2 = s.log_decay[bh % s.H] * kLog2e;
     const int64_t row0 = bh * s.L + t0;
+    auto load_rows = [&](int f0) { load_block(fss, static_cast<const T*>(s.fs) + row0 * s.F, kC, n, s.F, f0); };
+    auto load_state = [&](int f0) {
+        load_block(ms, s.st + ((bh * s.nc + c) * s.F + f0) * 64, 64, min(64, s.F - f0), 64, 0);
+        if (tid < 64) zs[tid] = norm && f0 + tid < s.F ? s.sz[(bh * s.nc + c) * s.F + f0 + tid] : 0.0f;
+    };
+    int f0 = group * 64;
+    if (n > i0) {
+        load_block(eqs, static_cast<const T*>(s.eq) + (row0 + i0) * 64, kRows, n - i0, 64, 0);
+        load_block(ps, static_cast<const T*>(s.es) + row0 * 64, kC, n, 64, 0);
+        loads_sent();
+        load_rows(f0);
+    }
+    after_previous_kernel();
+    if (n <= i0) return;
+    load_state(f0);
+    loads_sent();
     if (tid < kC) {
         const bool in = tid < n;
         pw[tid] = decay_pow(g2, tid);
         smul[tid] = in && s.s_mul ? s.s_mul[row0 + tid] : 1.0f;
         soff[tid] = in && s.s_off ? s.s_off[row0 + tid] : 0.0f;
     }
-    load_block(eqs, static_cast<const T*>(s.eq) + row0 * 64, n, 64, 0, nullptr);
-    load_block(ps, static_cast<const T*>(s.es) + row0 * 64, n, 64, 0, nullptr);
+    loads_done<1>();
     __syncthreads();
-    float p[4][4] = {};
-    mma_nt(p, eqs, ps, ty, tx);
+    float p[R][4] = {};
+    mma_nt<R>(p, eqs, ps, ty, tx);
     __syncthreads();
     // per query row: the score's scalars, the state's factor and the weight of its z column
-    float fac[4], zc[4];
+    float fac[R], zc[R];
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-        const int i = ty + 16 * a;
+    for (int a = 0; a < R; ++a) {
+        const int i = i0 + ty + 16 * a;
         const bool in = i < n;
         const float qm = in && s.q_mul ? s.q_mul[row0 + i] : 1.0f;
         const float qo = in && s.q_off ? s.q_off[row0 + i] : 0.0f;
@@ -396,34 +461,32 @@ __device__ __forceinline__ void out_e(const Sweep& s, float* sm, int64_t bh, T* 
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const int j = tx + 16 * b;
-            ps[i * kPitch + j] = score(p[a][b], i, j, n, s.rev, qo, soff[j], qm, smul, pw);
+            ps[(ty + 16 * a) * kPitch + j] = score(p[a][b], i, j, n, s.rev, qo, soff[j], qm, smul, pw);
         }
     }
     const bool vec = (s.F & 3) == 0;
-    for (int f0 = blockIdx.z * 64; f0 < s.F; f0 += gridDim.z * 64) {
-        __syncthreads();
-        load_block(fss, static_cast<const T*>(s.fs) + row0 * s.F, n, s.F, f0, nullptr);
-        load_block(ms, s.st + ((bh * s.nc + c) * s.F + f0) * 64, min(64, s.F - f0), 64, 0, nullptr);
-        if (tid < 64) zs[tid] = norm && f0 + tid < s.F ? s.sz[(bh * s.nc + c) * s.F + f0 + tid] : 0.0f;
+    for (;;) {
+        loads_done<0>();
         __syncthreads();
         // inter-chunk part with columns tx + 16 b; through shared memory to columns 4 tx + b
-        float t[4][4] = {}, acc[4][4] = {};
-        mma_nt(t, eqs, ms, ty, tx);
+        float t[R][4] = {};
+        float2 acc[R][2] = {};
+        mma_nt<R>(t, eqs, ms, ty, tx);
         __syncthreads();
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+        for (int a = 0; a < R; ++a)
 #pragma unroll
             for (int b = 0; b < 4; ++b)
                 ms[(ty + 16 * a) * kPitch + tx + 16 * b] = fac[a] * fmaf(zc[a], zs[tx + 16 * b], t[a][b]);
         __syncthreads();
-        mma_nn(acc, ps, fss, ty, tx);
+        mma_nn<R>(acc, ps, fss, ty, tx);
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
+        for (int a = 0; a < R; ++a) {
             const int i = ty + 16 * a, f = f0 + 4 * tx;
-            if (i >= n) continue;
+            if (i0 + i >= n) continue;
             const float4 m = *reinterpret_cast<const float4*>(ms + i * kPitch + 4 * tx);
-            const float4 w = make_float4(acc[a][0] + m.x, acc[a][1] + m.y, acc[a][2] + m.z, acc[a][3] + m.w);
-            T* dst = o + (row0 + i) * s.F + f;
+            const float4 w = make_float4(acc[a][0].x + m.x, acc[a][0].y + m.y, acc[a][1].x + m.z, acc[a][1].y + m.w);
+            T* dst = o + (row0 + i0 + i) * s.F + f;
             if (vec) {
                 if (f < s.F) st4(dst, w);
             } else {
@@ -433,25 +496,32 @@ __device__ __forceinline__ void out_e(const Sweep& s, float* sm, int64_t bh, T* 
                 if (f + 3 < s.F) stf(dst + 3, w.w);
             }
         }
+        f0 += groups * 64;
+        if (f0 >= s.F) break;
+        __syncthreads();
+        load_rows(f0);
+        load_state(f0);
+        loads_sent();
     }
 }
 
-// grid (nc, BH)
-template <typename T>
+// grid (nc, BH, 4 / R)
+template <typename T, int R>
 __global__ void __launch_bounds__(kNT) k_dec_fwd(Sweep s, T* o, float* den, bool norm, float eps)
 {
     extern __shared__ __align__(16) float sm[];
-    out_f(s, sm, blockIdx.y, o, den, norm, eps);
+    out_f<T, R>(s, sm, blockIdx.y, blockIdx.z, o, den, norm, eps);
 }
 
-// The three gradients side by side: grid (nc, 3 BH, column groups of the F-wide ones)
-template <typename T>
+// The three gradients side by side: grid (nc, 3 BH, 4 / R x column groups of the F-wide ones)
+template <typename T, int R>
 __global__ void __launch_bounds__(kNT) k_dec_grads(Sweep s, Sweep g, T* dphq, T* dphk, T* dv, int BH, bool norm)
 {
     extern __shared__ __align__(16) float sm[];
-    const int role = blockIdx.y / BH, bh = blockIdx.y % BH;
-    if (role < 2) out_e(role ? g : s, sm, bh, role ? dphk : dphq, norm);
-    else if (blockIdx.z == 0) out_f<T>(g, sm, bh, dv, nullptr, false, 0.0f);
+    constexpr int kParts = 4 / R;
+    const int role = blockIdx.y / BH, bh = blockIdx.y % BH, part = blockIdx.z % kParts, group = blockIdx.z / kParts;
+    if (role < 2) out_e<T, R>(role ? g : s, sm, bh, part, group, gridDim.z / kParts, role ? dphk : dphq, norm);
+    else if (group == 0) out_f<T, R>(g, sm, bh, part, dv, nullptr, false, 0.0f);
 }
 
 // Row statistics of the normalized backward: 16 bytes a lane, so 8 (bf16) or 16 (fp32) lanes a
@@ -483,8 +553,12 @@ __global__ void __launch_bounds__(256) k_dec_row_stats(const T* out, const T* do
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-constexpr size_t kSmemF = 3 * 64 * kPitch * sizeof(float), kSmemE = 4 * 64 * kPitch * sizeof(float),
-                 kSmemS = 2 * 64 * kPitch * sizeof(float);
+constexpr size_t kSmemS = 2 * 64 * kPitch * sizeof(float), kSmemO = 4 * 64 * kPitch * sizeof(float);
+// Up to this many CTAs, the outputs' kernels take half a chunk's queries each (R = 2): the
+// halves still find an SM each.  B1 H3 L512 F128 forward 20.5 us with halves against 22.8, with
+// 120 CTAs 30.8 / 34.9; but F64 22.6 / 20.5 there, and backward B1 H3 L512 F64 (72 CTAs)
+// 25.0 / 19.6, with 48 17.5 / 19.5.
+constexpr int64_t kFew = 64;
 
 // The states of a sweep, or of two at once.
 template <typename T>
@@ -503,13 +577,13 @@ cudaError_t states(const Sweep& s, const Sweep* g, int BH, bool chained, cudaStr
     return launch_in_chain(!chained, k_dec_scan, dim3(sb + zb, n), kNT, 0, st, s, g ? *g : s, BH, sb);
 }
 
-template <typename T>
-cudaError_t prepare_smem()
+template <typename K, typename... A>
+cudaError_t outputs(K* kernel, dim3 grid, cudaStream_t st, A... args)
 {
-    cudaError_t e = cudaFuncSetAttribute(k_dec_fwd<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemF);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_dec_grads<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemE);
-    return e;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemO);
+    if (e != cudaSuccess) return e;
+    TraceScope trace_("simt_decay_out", st);
+    return launch_in_chain(false, kernel, grid, kNT, kSmemO, st, args...);
 }
 
 struct Carve {
@@ -559,8 +633,7 @@ cudaError_t fwd_t(const DecayArgs& a, void* ws, cudaStream_t st)
 {
     const Carve c = carve(a, false, ws);
     const int BH = a.B * a.H;
-    cudaError_t e = prepare_smem<T>();
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     Sweep s = base(a, c);
     s.fq = a.phq;
     s.fs = a.phk;
@@ -570,9 +643,9 @@ cudaError_t fwd_t(const DecayArgs& a, void* ws, cudaStream_t st)
     s.last = a.S_out;
     s.last_z = a.z_out;
     if ((e = states<T>(s, nullptr, BH, false, st)) != cudaSuccess || s.nc == 0) return e;
-    TraceScope trace_("simt_decay_out", st);
-    return launch_in_chain(false, k_dec_fwd<T>, dim3(s.nc, BH), kNT, kSmemF, st, s, static_cast<T*>(a.out_w), a.den_w, a.norm,
-                           a.eps);
+    const bool few = static_cast<int64_t>(s.nc) * BH <= kFew;
+    return outputs(few ? k_dec_fwd<T, 2> : k_dec_fwd<T, 4>, dim3(s.nc, BH, few ? 2 : 1), st, s, static_cast<T*>(a.out_w),
+                   a.den_w, a.norm, a.eps);
 }
 
 template <typename T>
@@ -580,8 +653,7 @@ cudaError_t bwd_t(const DecayArgs& a, void* ws, cudaStream_t st)
 {
     const Carve c = carve(a, true, ws);
     const int BH = a.B * a.H;
-    cudaError_t e = prepare_smem<T>();
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     const bool stats = a.norm && a.L > 0;
     if (stats && (e = decay_row_stats(a, c.rz, c.r, st)) != cudaSuccess) return e;
     const float *rz = a.norm ? c.rz : nullptr, *r = a.norm ? c.r : nullptr;
@@ -613,10 +685,10 @@ cudaError_t bwd_t(const DecayArgs& a, void* ws, cudaStream_t st)
     // few CTAs: the column blocks of the F-wide outputs go to CTAs of their own
     const int nfb = (a.F + 63) / 64;
     const int64_t ctas = 3 * static_cast<int64_t>(BH) * s.nc;
-    const int zsplit = static_cast<int>(ctas >= 296 ? 1 : std::min<int64_t>(nfb, (296 + ctas - 1) / ctas));
-    TraceScope trace_("simt_decay_out", st);
-    return launch_in_chain(false, k_dec_grads<T>, dim3(s.nc, 3 * BH, zsplit), kNT, kSmemE, st, s, g, static_cast<T*>(a.dphq),
-                           static_cast<T*>(a.dphk), static_cast<T*>(a.dv), BH, a.norm);
+    const int groups = static_cast<int>(ctas >= 296 ? 1 : std::min<int64_t>(nfb, (296 + ctas - 1) / ctas));
+    const bool few = ctas * groups <= kFew;
+    return outputs(few ? k_dec_grads<T, 2> : k_dec_grads<T, 4>, dim3(s.nc, 3 * BH, few ? 2 * groups : groups), st, s, g,
+                   static_cast<T*>(a.dphq), static_cast<T*>(a.dphk), static_cast<T*>(a.dv), BH, a.norm);
 }
 
 }  // namespace
