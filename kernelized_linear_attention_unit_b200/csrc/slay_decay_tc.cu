@@ -26,7 +26,7 @@
 // chunk, which is why accumulators are as wide as tensor memory allows; P~ is read from tensor
 // memory.  The chain of a chunk (scores, masking, state sum, its bf16 copy, the next scores)
 // takes 8000 to 9000 clocks: forward B32 H12 L1024 F256 in 104 us, 4.9 TB/s, 74% of the copy
-// bandwidth; with fewer (b, h) than SMs the sequence is cut into segments, whose sums
+// bandwidth (tensor pipe 32% active); with fewer (b, h) than SMs the sequence is cut into segments, whose sums
 // (k_tc_dec<kState>) read the F side once more.  Measured alternatives: 512 threads with four
 // state warps in kOutF, too, 121 against 104 us; MMA loops not unrolled 126 us; roles chosen at
 // run time 162 us (the code outgrew the instruction cache).
@@ -1107,8 +1107,11 @@ bool map_rows(CUtensorMap* m, const void* base, int cols, int L, int64_t BH, boo
               out ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a sweep is cut: blocks of at most `most` features, and segments of the sequence so that
-// the CTAs fill the GPU (one a SM).
+// How a sweep is cut: blocks of at most `most` features, and as many segments of the sequence
+// as give each CTA an SM.  More of them cost more than they balance: forward B4 H8 L2048 F256
+// 40 us with four, 54 with eight; backward B2 H16 L8192 F512 657 with four, 694 with nine
+// (1.95 waves instead of 0.86); ragged batches too, forward B8 H16 L1500 F128 43 with one, 56
+// with two, backward B8 H8 L1111 F128 76 with two, 82 with three.
 struct Plan {
     int nfb, fw, nseg;
     int64_t BH;
@@ -1220,9 +1223,9 @@ P base(const DecayArgs& a, const Plan& c, int* err)
 
 // What the output sweeps start from, and the state that the walk leaves.  Up to kMaxSums
 // segments, each sweep adds up the sums of the segments before its own (66 KB each from L2, at
-// F = 256) and the one that walks last writes the state; beyond, a scan kernel does both.  B200, forward at F = 256:
-// four segments (B4 H8 L2048) 44 us against 47 with the scan, nine (B1 H16 L16384) 137 against
-// 127.
+// F = 256) and the one that walks last writes the state; beyond, a scan kernel does both.
+// Forward at F = 256: four segments (B4 H8 L2048) 40 us against 44 with the scan, nine
+// (B1 H16 L16384) 128 against 118.
 constexpr int kMaxSums = 4;
 cudaError_t segment_states(const DecayArgs& a, const Plan& c, const Carve& k, P& p, const CUtensorMap& fs,
                            const CUtensorMap& es, bool rev, const float* first, const float* first_z, float* last,
