@@ -363,8 +363,8 @@ slay_status slay_linear_attn_fwd(const void* phq, const void* phk, const void* v
  * out : device [B,H,L,Dv] in dt;  den : device [B,H,L] fp32 or NULL (without eps; NULL when
  *             normalize == 0).  eps is ignored when normalize == 0.
  * workspace : slay_workspace_bytes(SLAY_OP_DECAY_FWD, dt, B, H, L, 64, Dv, 1, F) bytes; it
- *             serves one call at a time.
- * Outputs share no memory with inputs, but for the states.  A token of a sequence that is not
+ *             serves one call at a time, captured graphs that hold it included.
+ * Outputs share no memory with inputs, but that S_out, z_out may be S_in, z_in.  A token of a sequence that is not
  * finite may reach every row of its 128-token chunk.  B*H <= 21845.
  * bf16 with F % 8 == 0, F <= 512 runs on tensor cores (SLAY_PATH_TC_CONTRACTION): fp32
  * accumulation; the masked scores and the state's operand are rounded to bf16, den and the

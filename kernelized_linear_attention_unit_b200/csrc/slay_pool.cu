@@ -20,6 +20,7 @@ namespace cg = cooperative_groups;
 constexpr int kNT = 256;
 constexpr int kNumSMs = 148;
 constexpr int kRows = 4;        // rows of S a decode thread loads ahead
+constexpr int kCopySmem = 128 * 1024;   // of a copying CTA at most: 32 KiB of lists, then 64 KiB of table or stage for 4096 pairs
 
 __device__ __forceinline__ float ldf(const float* p) { return *p; }
 __device__ __forceinline__ float ldf(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -277,7 +278,9 @@ cudaError_t state_copy(const CopyArgs& a, cudaStream_t st)
     const int nZ = static_cast<int>((uZ + wZ - 1) / wZ);
     const size_t stage = static_cast<size_t>(a.n) * std::max(wS, wZ) * 16;
     const size_t smem = lists + std::max(stage, 2 * static_cast<size_t>(table) * sizeof(int));
-    cudaError_t e = cudaFuncSetAttribute(k_state_copy, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // (the same limit whatever the call needs: another host thread may set it in between)
+    if (smem > kCopySmem) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(k_state_copy, cudaFuncAttributeMaxDynamicSharedMemorySize, kCopySmem);
     if (e != cudaSuccess) return e;
     int per_sm = 1;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_state_copy, kNT, smem);

@@ -12,6 +12,7 @@ Tolerances.  u is the output type's half step (2^-8 bf16, 2^-24 fp32).
     half step have an rms of u / sqrt(3); four of them 2 u / sqrt(3) < 1.2 u -> 1.5 u in bf16;
     1e-5 for fp32 outputs, the library's bar.
 """
+import concurrent.futures
 import math
 
 import pytest
@@ -191,6 +192,16 @@ def test_backward(B, H, L, F, dt, norm, ragged, state):
     for k in ("dS_in", "dz_in"):
         if got[k] is not None:
             _ok(k, got[k], want[k], mag[k], dt, L, L > 16 and not (norm and dt == "f32"))
+
+
+# CUDA cores: half chunks and whole ones a block, one and several blocks of features, grouped and not
+@pytest.mark.parametrize("B,H,L,F,dt,norm,ragged,state", [
+    (8, 3, 700, 96, "f32", True, True, True), (8, 3, 500, 36, "f32", False, True, True),
+    (1, 2, 1000, 200, "f32", True, False, True), (1, 1, 200, 64, "f32", True, False, True),
+    (1, 1, 97, 130, "bf16", True, False, True), (3, 5, 400, 70, "bf16", False, True, True)])
+def test_cuda_cores_few_and_many_chunks(B, H, L, F, dt, norm, ragged, state):
+    test_forward(B, H, L, F, dt, norm, ragged, state)
+    test_backward(B, H, L, F, dt, norm, ragged, state)
 
 
 def test_gradients_against_differences():
@@ -441,6 +452,28 @@ def test_state_copy(slots, H, F, n, z, seed):
         assert torch.equal(otherZ, wOZ) and torch.equal(Z, wZ)
 
 
+def test_copies_of_two_host_threads():
+    """Calls of different sizes from two threads, each on its own pools and stream."""
+    def work(seed, n, slots, H, F):
+        g = _gen(seed)
+        S, Z = _randn(g, slots, H, F, 64), _randn(g, slots, H, F)
+        src = torch.randint(0, slots, (n,), generator=g, device="cuda", dtype=torch.int32)
+        dst = torch.randperm(slots, generator=g, device="cuda")[:n].int()
+        want, wantZ = _copy_want(S, src.tolist(), S, dst.tolist()), _copy_want(Z, src.tolist(), Z, dst.tolist())
+        S2, Z2, st = torch.empty_like(S), torch.empty_like(Z), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            for _ in range(200):
+                S2.copy_(S), Z2.copy_(Z)
+                bd.slay_state_copy(S2, Z2, src, S2, Z2, dst)
+        st.synchronize()
+        return torch.equal(S2, want) and torch.equal(Z2, wantZ)
+
+    with concurrent.futures.ThreadPoolExecutor(2) as ex:
+        runs = [ex.submit(work, 31, 3, 8, 2, 64), ex.submit(work, 32, 2000, 2000, 1, 16)]
+        assert all(r.result() for r in runs)
+
+
 def test_swap_cycle_and_clear():
     g = _gen(11)
     S, Z = _randn(g, 5, 2, 64, 64), _randn(g, 5, 2, 64)
@@ -449,6 +482,47 @@ def test_swap_cycle_and_clear():
     bd.slay_state_copy(S, Z, i(1, 2, 0, -1), S, Z, i(0, 1, 2, 4))
     for pool, old in ((S, S0), (Z, Z0)):
         assert torch.equal(pool[:3], old[[1, 2, 0]]) and torch.equal(pool[3], old[3]) and not pool[4].any()
+
+
+# ------------------------------------------------------------------ past 32 bits
+def test_pool_offsets_past_32_bits():
+    """Slots that start beyond 2^31 elements of a pool step and move as those of a small one."""
+    H, F, n = 16, 512, 4200
+    g = _gen(21)
+    small, small_z = _randn(g, 3, H, F, 64), torch.exp(_randn(g, 3, H, F))
+    pool, pool_z = torch.zeros(n, H, F, 64, device="cuda"), torch.zeros(n, H, F, device="cuda")
+    assert (n - 2) * H * F * 64 > 2 ** 31
+    i32 = lambda *x: torch.tensor(x, device="cuda", dtype=torch.int32)  # noqa: E731
+    bd.slay_state_copy(small, small_z, i32(0, 1, 2), pool, pool_z, i32(n - 1, 0, n - 2))
+    q, k = _features(g, "bf16", True, 2, H, F), _features(g, "bf16", True, 2, H, F)
+    v, ld = _randn(g, 2, H, 64).bfloat16(), _decays(H, "slow")
+    a, b = torch.empty_like(v), torch.empty_like(v)
+    bd.slay_decay_decode_step(q, k, v, ld, pool, pool_z, a, slots=i32(n - 1, n - 2))
+    bd.slay_decay_decode_step(q, k, v, ld, small, small_z, b, slots=i32(0, 2))
+    bd.slay_state_copy(pool, pool_z, i32(n - 2, -1), pool, pool_z, i32(n - 3, 0))
+    assert torch.equal(a, b)
+    assert torch.equal(pool[n - 1], small[0]) and torch.equal(pool[n - 2], small[2]) and torch.equal(pool[n - 3], small[2])
+    assert torch.equal(pool_z[n - 1], small_z[0]) and torch.equal(pool_z[n - 3], small_z[2])
+    assert not pool[0].any() and not pool[1].any() and not pool[n - 4].any()
+
+
+@pytest.mark.parametrize("B,H,L,F,dt", [(2100, 1, 2048, 512, "bf16"), (1100, 4, 1024, 512, "f32")])
+def test_batch_offsets_past_32_bits(B, H, L, F, dt):
+    """A batch of more than 2^31 feature elements, every sequence the same: so are its results."""
+    assert B * H * L * F > 2 ** 31
+    c, g = _case(1, H, L, F, dt, False, False, False, seed=22, kind="slow")
+    dout = _randn(g, 1, H, L, 64).to(TDT[dt])
+    many = lambda x: x.expand(B, *x.shape[1:]).contiguous()  # noqa: E731
+    q, k, v, do = many(c["phq"]), many(c["phk"]), many(c["v"]), many(dout)
+    out, dq, dk, dv = torch.zeros_like(v), torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    bd.slay_decay_attn_fwd(q, k, v, c["log_decay"], out, normalize=False)
+    bd.slay_decay_attn_bwd(q, k, v, c["log_decay"], do, dq, dk, dv, normalize=False)
+    want, mag = ref.forward(**c)
+    _ok("out", out[:1], want["out"], mag["out"], dt, L + F)
+    for x in (out, dq, dk, dv):
+        assert x[0].any() and all(torch.equal(x[b], x[0]) for b in range(1, B))
+    del q, k, v, do, out, dq, dk, dv, x
+    torch.cuda.empty_cache()
 
 
 # ------------------------------------------------------------- as a server would use them
