@@ -136,6 +136,14 @@ struct P {
     int H, L, F, nseg, nfb, fw, fb0;
     int seg0, nsl;                                // segments of this launch: seg0 .. seg0 + nsl - 1
     int z_state;                                  // keep z (kOutF backward: only where it is wanted)
+    // kState in pairs: the direction, and a second walk of the same launch, from CTA n0 on (its
+    // operands are the maps tfq and teq)
+    int rev, n0;
+    struct Walk {
+        const float *s_mul, *s_off;
+        float *last, *last_z;
+        int rev, nseg, seg0, nsl;
+    } second;
     int* err;
 };
 
@@ -188,9 +196,9 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-// kRev: the sweep walks the chunks backward.  kNorm: the normalized form, whose backward puts
+// kRev: the sweep walks the chunks backward (kPair: as each of the two walks says).  kNorm: the normalized form, whose backward puts
 // its row scalars on the state tokens (kRev) or on the query tokens (kOutE forward).
-template <int kMode, bool kRev, bool kNorm>
+template <int kMode, bool kRev, bool kNorm, bool kPair>
 __global__ void __launch_bounds__(threads(kMode), 1)
 k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtensorMap tfq,
          const __grid_constant__ CUtensorMap tes, const __grid_constant__ CUtensorMap teq,
@@ -214,18 +222,22 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
 
     // this CTA's feature block, segment and sequence
     int x = blockIdx.x;
+    const bool second = kPair && x >= p.n0;
+    if (second) x -= p.n0;
+    const bool rev = kPair ? (second ? p.second.rev : p.rev) != 0 : kRev;
+    const int nseg = second ? p.second.nseg : p.nseg, nsl = second ? p.second.nsl : p.nsl;
     const int fb = kMode == kOutF ? p.fb0 : x % p.nfb;
     if (kMode != kOutF) x /= p.nfb;
-    const int seg = p.seg0 + x % p.nsl, bh = x / p.nsl;
+    const int seg = (second ? p.second.seg0 : p.seg0) + x % nsl, bh = x / nsl;
     const int f0 = fb * p.fw, fv = min(p.fw, p.F - f0);
     const int ns = (fv + 63) >> 6, nsE = (ns + 1) & ~1;   // 64-feature slices; as whole pairs
     const int len = p.lengths ? min(max(p.lengths[bh / p.H], 0), p.L) : p.L;
     const int nch = (len + kT - 1) / kT;
-    auto seg_lo = [&](int s) { return s * nch / p.nseg; };   // (at most 32768 chunks, 148 segments)
+    auto seg_lo = [&](int s) { return s * nch / nseg; };   // (at most 32768 chunks, 148 segments)
     const int c_lo = seg_lo(seg), count = seg_lo(seg + 1) - c_lo;
     // whether the state that leaves this CTA's walk is an output
-    const bool leaves = p.last && (kMode == kState || seg == (kRev ? 0 : p.nseg - 1));
-    auto chunk_of = [&](int i) { return kRev ? c_lo + count - 1 - i : c_lo + i; };
+    const bool leaves = p.last && (kMode == kState || seg == (kRev ? 0 : nseg - 1));
+    auto chunk_of = [&](int i) { return rev ? c_lo + count - 1 - i : c_lo + i; };
     const float g2 = p.log_decay[bh % p.H] * kLog2e;
     // limbs of the weighted rows: three where the fp32 state leaves the call, two (2^-17) where
     // only its bf16 copy is read; without decay and row scalars the weights are 1, one is exact
@@ -257,8 +269,8 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
         for (int i = 0; i < B_NUM; ++i)
             mbar_init(&bar[i], i >= B_YF && i < B_YF + 4 ? (kSplit ? 4 : 8) : i == B_PT || i == B_OE || i == B_OE + 1 ? 8 : 1);
         mbar_fence_init();
-        tma_prefetch_desc(&tfs);
-        tma_prefetch_desc(&tes);
+        tma_prefetch_desc(second ? &tfq : &tfs);
+        tma_prefetch_desc(second ? &teq : &tes);
         if (kMode == kOutF) tma_prefetch_desc(&tfq);
         if (kMode == kOutE) tma_prefetch_desc(&teq);
     }
@@ -290,7 +302,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                 auto load_e = [&] {   // the 64-wide rows
                     if (i >= kEs) wait_k(B_ESE + b, i / kEs - 1);
                     mbar_arrive_expect_tx(&bar[B_ESF + b], kMode == kOutE ? 2 * kTile : kTile);
-                    tma_load_3d(sm + Lo.es + b * kTile, &tes, &bar[B_ESF + b], 0, t0, bh);
+                    tma_load_3d(sm + Lo.es + b * kTile, second ? &teq : &tes, &bar[B_ESF + b], 0, t0, bh);
                     if (kMode == kOutE) tma_load_3d(sm + Lo.eq + b * kTile, &teq, &bar[B_ESF + b], 0, t0, bh);
                 };
                 if (kMode != kOutF || i == 0) load_e();
@@ -299,7 +311,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
                     if (u >= 4) wait_k(B_FSE + sl, (u >> 2) - 1);
                     if (s < ns) {
                         mbar_arrive_expect_tx(&bar[B_FSF + sl], kTile);
-                        tma_load_3d(sm + Lo.fs + sl * kSlot, &tfs, &bar[B_FSF + sl], f0 + 64 * s, t0, bh);
+                        tma_load_3d(sm + Lo.fs + sl * kSlot, second ? &tfq : &tfs, &bar[B_FSF + sl], f0 + 64 * s, t0, bh);
                     } else {
                         mbar_arrive(&bar[B_FSF + sl]);   // the second half of the last pair: not read
                     }
@@ -509,7 +521,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
         float* soff = reinterpret_cast<float*>(sm + Lo.soff);
         float* dsum = reinterpret_cast<float*>(sm + Lo.dsum);
         float* zf = reinterpret_cast<float*>(sm + Lo.zf);
-        const int64_t sidx = static_cast<int64_t>(bh) * p.nseg + seg;
+        const int64_t sidx = static_cast<int64_t>(bh) * nseg + seg;
         // the scalars of four query / state tokens: off the raw scores, onto the weights
         auto scale = [&](int par, int j, float2 off, float2& s0, float2& s1, float2& w0, float2& w1) {
             if (kRows) {
@@ -730,9 +742,9 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
         } else {
             if (p.first) add_state(p.first, p.first_z, bh, 1.0f, false);
             if (p.sums)
-                for (int i = 0; i < (kRev ? p.nseg - 1 - seg : seg); ++i) {
-                    const int s = kRev ? p.nseg - 1 - i : i;
-                    add_state(p.sums, p.sums_z, static_cast<int64_t>(bh) * p.nseg + s,
+                for (int i = 0; i < (kRev ? nseg - 1 - seg : seg); ++i) {
+                    const int s = kRev ? nseg - 1 - i : i;
+                    add_state(p.sums, p.sums_z, static_cast<int64_t>(bh) * nseg + s,
                               decay_pow(g2, max(min(seg_lo(s + 1) * kT, len) - seg_lo(s) * kT, 0)), true);
                 }
         }
@@ -782,9 +794,10 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
             const int t0 = chunk_of(i) * kT, n = min(kT, len - t0), eb = i % kEs;
             const bool in = row < n;
             const int64_t grow = static_cast<int64_t>(bh) * p.L + t0 + row;
-            const float mul = kCols && in ? p.s_mul[grow] : 1.0f;
-            const float off = kCols && in ? p.s_off[grow] : 0.0f;
-            const float w = in ? decay_pow(g2, kRev ? row + 1 : n - 1 - row) : 0.0f;
+            const bool cols = kPair ? kNorm && rev : kCols;   // row scalars on the state tokens
+            const float mul = cols && in ? (second ? p.second.s_mul : p.s_mul)[grow] : 1.0f;
+            const float off = cols && in ? (second ? p.second.s_off : p.s_off)[grow] : 0.0f;
+            const float w = in ? decay_pow(g2, rev ? row + 1 : n - 1 - row) : 0.0f;
             const float a = w * mul;
             const uint32_t ybase = sbase + kY + (kMode == kState ? eb * 4 * kTile : 0);
             wait_k(B_ESF + eb, i / kEs);
@@ -822,7 +835,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
             if (half == 0) {
                 if (has_z) {
                     uint16_t l[3];
-                    limbs3(kCols ? -a * off : w, l);
+                    limbs3(cols ? -a * off : w, l);
                     if (kMode == kState) {
                         const uint32_t lo = l[0] | (static_cast<uint32_t>(l[1]) << 16);
                         st_shared_v4(ybase + 3 * kTile + sw128_off(row, 0), lo, l[2], 0u, 0u);
@@ -1015,16 +1028,17 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
         }
         if (leaves) {
             const int64_t at = kMode == kState ? sidx : bh;
+            float *const last = second ? p.second.last : p.last, *const last_z = second ? p.second.last_z : p.last_z;
 #pragma unroll
             for (int b = 0; b < kNb; ++b) {
                 const int f = 128 * b + row;
                 if (f >= fv) continue;
-                float4* dst = kMode == kState ? reinterpret_cast<float4*>(p.last + at * sums_floats(p.F)) + sums_at(f0 + f, 8 * half)
-                                              : reinterpret_cast<float4*>(p.last + (at * p.F + f0 + f) * 64 + 32 * half);
+                float4* dst = kMode == kState ? reinterpret_cast<float4*>(last + at * sums_floats(p.F)) + sums_at(f0 + f, 8 * half)
+                                              : reinterpret_cast<float4*>(last + (at * p.F + f0 + f) * 64 + 32 * half);
 #pragma unroll
                 for (int c = 0; c < kW / 4; ++c)
                     dst[c * (kMode == kState ? 128 : 1)] = make_float4(run[b][4 * c], run[b][4 * c + 1], run[b][4 * c + 2], run[b][4 * c + 3]);
-                if (has_zrow(b) && p.last_z) p.last_z[at * p.F + f0 + f] = zrun[b];
+                if (has_zrow(b) && last_z) last_z[at * p.F + f0 + f] = zrun[b];
             }
         }
         }
@@ -1143,8 +1157,14 @@ Plan plan_q(const DecayArgs& a)
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// Sums (or starting states) of a walk's segments.
+struct Segs {
+    float *st, *sz;
+};
+
 struct Carve {
-    float *st, *sz, *in, *in_z, *part, *part_den, *rz, *r;
+    Segs walk, walk_q;   // of the walk that the 64-wide output shares, and of dphq's
+    float *in, *in_z, *part, *part_den, *rz, *r;
     size_t bytes;
 };
 
@@ -1160,10 +1180,16 @@ Carve carve(const DecayArgs& a, bool bwd, void* ws)
     Carve k{};
     const Plan c = plan_f(a);
     const size_t rows = static_cast<size_t>(c.BH) * a.L;
-    const int nseg = bwd ? std::max(c.nseg, plan_q(a).nseg) : c.nseg;
-    if (nseg > 1) {
-        k.st = take(static_cast<size_t>(c.BH) * nseg * sums_floats(a.F));
-        k.sz = take(static_cast<size_t>(c.BH) * nseg * a.F);
+    auto segs = [&](int nseg) {
+        Segs s{};
+        if (nseg > 1) {
+            s.st = take(static_cast<size_t>(c.BH) * nseg * sums_floats(a.F));
+            s.sz = take(static_cast<size_t>(c.BH) * nseg * a.F);
+        }
+        return s;
+    };
+    k.walk = segs(c.nseg);
+    if (c.nseg > 1) {
         k.in = take(static_cast<size_t>(c.BH) * a.F * 64);
         k.in_z = take(static_cast<size_t>(c.BH) * a.F);
     }
@@ -1175,21 +1201,24 @@ Carve carve(const DecayArgs& a, bool bwd, void* ws)
     if (bwd) {
         k.rz = take(rows);
         k.r = take(rows);
+        DecayArgs other = a;    // (the size of a workspace serves either form)
+        other.norm = !a.norm;
+        k.walk_q = segs(std::max(plan_q(a).nseg, plan_q(other).nseg));
     }
     k.bytes = o;
     return k;
 }
 
-template <int kMode, bool kRev, bool kNorm>
+template <int kMode, bool kRev, bool kNorm, bool kPair = false>
 cudaError_t launch1(const CUtensorMap& fs, const CUtensorMap& fq, const CUtensorMap& es, const CUtensorMap& eq,
                     const CUtensorMap& out, const P& p, const Plan& c, bool& chained, cudaStream_t st)
 {
     constexpr size_t smem = layout(kMode).total + 1024;
     static_assert(smem <= 232448, "shared memory of one CTA");
-    const auto kernel = k_tc_dec<kMode, kRev, kNorm>;
+    const auto kernel = k_tc_dec<kMode, kRev, kNorm, kPair>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t grid = c.BH * p.nsl * (kMode == kOutF ? 1 : p.nfb);
+    const int64_t grid = c.BH * (p.nsl + (kPair ? p.second.nsl : 0)) * (kMode == kOutF ? 1 : p.nfb);
     const bool first = !chained;
     chained = true;
     return launch_in_chain(first, +kernel, dim3(static_cast<unsigned>(grid)), threads(kMode), smem, st, fs, fq, es, eq, out, p);
@@ -1201,6 +1230,9 @@ cudaError_t launch(const char* name, const CUtensorMap& fs, const CUtensorMap& f
                    bool& chained, cudaStream_t st)
 {
     TraceScope trace_(name, st);
+    if constexpr (kMode == kState)
+        if (p.second.nsl > 0)
+            return norm ? launch1<kMode, false, true, true>(fs, fq, es, eq, out, p, c, chained, st) : launch1<kMode, false, false, true>(fs, fq, es, eq, out, p, c, chained, st);
     if (rev) return norm ? launch1<kMode, true, true>(fs, fq, es, eq, out, p, c, chained, st) : launch1<kMode, true, false>(fs, fq, es, eq, out, p, c, chained, st);
     return norm ? launch1<kMode, false, true>(fs, fq, es, eq, out, p, c, chained, st) : launch1<kMode, false, false>(fs, fq, es, eq, out, p, c, chained, st);
 }
@@ -1227,50 +1259,90 @@ P base(const DecayArgs& a, const Plan& c, int* err)
 // Forward at F = 256: four segments (B4 H8 L2048) 40 us against 44 with the scan, nine
 // (B1 H16 L16384) 128 against 118.
 constexpr int kMaxSums = 4;
-cudaError_t segment_states(const DecayArgs& a, const Plan& c, const Carve& k, P& p, const CUtensorMap& fs,
-                           const CUtensorMap& es, bool rev, const float* first, const float* first_z, float* last,
-                           float* last_z, bool& chained, cudaStream_t st)
+
+// A walk whose segments' states are wanted.
+struct Start {
+    const Plan* c;
+    Segs segs;
+    P* p;                          // its sweeps' parameters
+    const CUtensorMap *fs, *es;
+    bool rev;
+    const float *first, *first_z;
+    float *last, *last_z;
+    bool scan() const { return c->nseg > kMaxSums; }
+    int summed() const { return scan() ? c->nseg : c->nseg - 1; }   // (without a scan nobody adds the last segment's)
+};
+
+// Two walks' sums come from one launch where its CTAs still find an SM each: backward B8 H8
+// L1111 F128 69 us, 76 one after the other; beyond, the sweep that follows a walk's own launch
+// finds its rows in L2, B1 H8 L16000 F256 170 us against 181.
+bool together(const DecayArgs& a, const Start& x, const Start& y)
 {
-    p.first = first;
-    p.first_z = first_z;
-    p.last = last;
-    p.last_z = last_z;
-    if (c.nseg == 1) return cudaSuccess;
-    const bool scan = c.nseg > kMaxSums;
-    if (!scan && first && (last == first || (last_z && last_z == first_z))) {
-        // in place: the CTAs read a copy, one of them writes the state while others start
-        const size_t n = static_cast<size_t>(c.BH) * a.F * sizeof(float);
-        cudaError_t e = cudaMemcpyAsync(k.in, first, n * 64, cudaMemcpyDeviceToDevice, st);
-        if (e == cudaSuccess && first_z) e = cudaMemcpyAsync(k.in_z, first_z, n, cudaMemcpyDeviceToDevice, st);
-        if (e != cudaSuccess) return e;
-        p.first = k.in;
-        p.first_z = first_z ? k.in_z : nullptr;
-        chained = false;                     // the next kernel follows a copy
+    const Plan cs = plan(a, kMaxFw, true);
+    return x.c->nseg > 1 && y.c->nseg > 1 && cs.BH * cs.nfb * (x.summed() + y.summed()) <= kNumSMs;
+}
+
+// For one walk or two.
+cudaError_t segment_states(const DecayArgs& a, const Carve& k, Start* const* walks, int n, bool& chained, cudaStream_t st)
+{
+    Start* cut[2];
+    int m = 0;
+    for (int i = 0; i < n; ++i) {
+        Start& w = *walks[i];
+        P& p = *w.p;
+        p.first = w.first;
+        p.first_z = w.first_z;
+        p.last = w.last;
+        p.last_z = w.last_z;
+        if (w.c->nseg == 1) continue;
+        if (!w.scan() && w.first && (w.last == w.first || (w.last_z && w.last_z == w.first_z))) {
+            // in place: the CTAs read a copy, one of them writes the state while others start
+            const size_t floats = static_cast<size_t>(w.c->BH) * a.F * sizeof(float);
+            cudaError_t e = cudaMemcpyAsync(k.in, w.first, floats * 64, cudaMemcpyDeviceToDevice, st);
+            if (e == cudaSuccess && w.first_z) e = cudaMemcpyAsync(k.in_z, w.first_z, floats, cudaMemcpyDeviceToDevice, st);
+            if (e != cudaSuccess) return e;
+            p.first = k.in;
+            p.first_z = w.first_z ? k.in_z : nullptr;
+            chained = false;             // the next kernel follows a copy
+        }
+        cut[m++] = &w;
     }
-    P q = p;
+    if (m == 0) return cudaSuccess;
+    auto walk = [&](const Start& w) {
+        return P::Walk{w.p->s_mul, w.p->s_off, w.segs.st, w.segs.sz, w.rev ? 1 : 0, w.c->nseg,
+                       w.rev ? w.c->nseg - w.summed() : 0, w.summed()};
+    };
     const Plan cs = plan(a, kMaxFw, true);   // (the sums go by blocks of 256 whatever the sweep's)
+    P q = *cut[0]->p;
     q.nfb = cs.nfb;
     q.fw = cs.fw;
     q.first = q.first_z = nullptr;
-    q.last = k.st;
-    q.last_z = k.sz;
-    if (!scan) {                             // nobody adds the last segment's
-        q.nsl = c.nseg - 1;
-        q.seg0 = rev ? 1 : 0;
+    const P::Walk w0 = walk(*cut[0]);
+    q.last = w0.last;
+    q.last_z = w0.last_z;
+    q.rev = w0.rev;
+    q.nsl = w0.nsl;
+    q.seg0 = w0.seg0;
+    q.n0 = static_cast<int>(cs.BH * w0.nsl * cs.nfb);
+    if (m == 2) q.second = walk(*cut[1]);
+    const Start& o = *cut[m - 1];
+    cudaError_t e = launch<kState>("tc_decay_state", *cut[0]->fs, *o.fs, *cut[0]->es, *o.es, *cut[0]->fs, q, cs, cut[0]->rev, a.norm, chained, st);
+    for (int i = 0; i < m && e == cudaSuccess; ++i) {
+        const Start& w = *cut[i];
+        P& p = *w.p;
+        if (!w.scan()) {
+            p.sums = w.segs.st;
+            p.sums_z = w.segs.sz;
+            continue;
+        }
+        TraceScope trace_("decay_seg_scan", st);
+        e = launch_in_chain(false, k_dec_seg_scan, dim3(static_cast<unsigned>((sums_floats(a.F) / 4 + a.F + 255) / 256), static_cast<unsigned>(w.c->BH)),
+                            256, 0, st, w.segs.st, a.norm ? w.segs.sz : nullptr, w.first, w.first_z, w.last, w.last_z, a.F,
+                            w.c->nseg, w.rev, a.log_decay, a.lengths, a.H, a.L);
+        p.starts = w.segs.st;
+        p.starts_z = w.segs.sz;
+        p.last = p.last_z = nullptr;
     }
-    cudaError_t e = launch<kState>("tc_decay_state", fs, fs, es, es, fs, q, cs, rev, a.norm, chained, st);
-    if (e != cudaSuccess) return e;
-    if (!scan) {
-        p.sums = k.st;
-        p.sums_z = k.sz;
-        return cudaSuccess;
-    }
-    TraceScope trace_("decay_seg_scan", st);
-    e = launch_in_chain(false, k_dec_seg_scan, dim3(static_cast<unsigned>((sums_floats(a.F) / 4 + a.F + 255) / 256), static_cast<unsigned>(c.BH)), 256, 0, st, k.st,
-                        a.norm ? k.sz : nullptr, first, first_z, last, last_z, a.F, c.nseg, rev, a.log_decay, a.lengths, a.H, a.L);
-    p.starts = k.st;
-    p.starts_z = k.sz;
-    p.last = p.last_z = nullptr;
     return e;
 }
 
@@ -1308,7 +1380,8 @@ cudaError_t decay_tc_fwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
         return cudaErrorInvalidValue;
     P p = base(a, c, err);
     bool chained = false;   // whether a kernel of this call runs before
-    cudaError_t e = segment_states(a, c, k, p, mk, mv, false, a.S_in, a.z_in, a.S_out, a.z_out, chained, st);
+    Start w{&c, k.walk, &p, &mk, &mv, false, a.S_in, a.z_in, a.S_out, a.z_out}, *walks[] = {&w};
+    cudaError_t e = segment_states(a, k, walks, 1, chained, st);
     if (e != cudaSuccess) return e;
     p.o = static_cast<__nv_bfloat16*>(a.out_w);
     p.den = a.den_w;
@@ -1329,15 +1402,18 @@ cudaError_t decay_tc_bwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
     if (e != cudaSuccess) return e;
     const float *rz = a.norm ? k.rz : nullptr, *r = a.norm ? k.r : nullptr;
     P s = base(a, cq, err);   // dphq from the states before each token
-    if ((e = segment_states(a, cq, k, s, mk, mv, false, a.S_in, a.z_in, nullptr, nullptr, chained, st)) != cudaSuccess) return e;
+    P g = base(a, c, err);    // dphk and dv from the states after each token
+    g.s_mul = rz;
+    g.s_off = r;
+    Start before{&cq, k.walk_q, &s, &mk, &mv, false, a.S_in, a.z_in, nullptr, nullptr};
+    Start after{&c, k.walk, &g, &mq, &mo, true, a.dS_out, a.dz_out, a.dS_in, a.dz_in}, *walks[] = {&after, &before};
+    const bool both = together(a, after, before);
+    if ((e = segment_states(a, k, both ? walks : walks + 1, both ? 2 : 1, chained, st)) != cudaSuccess) return e;
     s.q_mul = rz;
     s.q_off = r;
     s.o = static_cast<__nv_bfloat16*>(a.dphq);
     if ((e = launch<kOutE>("tc_decay_out_e", mk, mk, mv, mo, mdq, s, cq, false, a.norm, chained, st)) != cudaSuccess) return e;
-    P g = base(a, c, err);   // dphk and dv from the states after each token
-    g.s_mul = rz;
-    g.s_off = r;
-    if ((e = segment_states(a, c, k, g, mq, mo, true, a.dS_out, a.dz_out, a.dS_in, a.dz_in, chained, st)) != cudaSuccess) return e;
+    if (!both && (e = segment_states(a, k, walks, 1, chained, st)) != cudaSuccess) return e;
     P w = g;                 // (the state that the walk leaves is dv's sweep to write)
     w.last = w.last_z = nullptr;
     w.o = static_cast<__nv_bfloat16*>(a.dphk);
