@@ -198,11 +198,9 @@ __device__ __forceinline__ bool elect_one()
 
 // kRev: the sweep walks the chunks backward (kPair: as each of the two walks says).  kNorm: the normalized form, whose backward puts
 // its row scalars on the state tokens (kRev) or on the query tokens (kOutE forward).
-template <int kMode, bool kRev, bool kNorm, bool kPair>
-__global__ void __launch_bounds__(threads(kMode), 1)
-k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtensorMap tfq,
-         const __grid_constant__ CUtensorMap tes, const __grid_constant__ CUtensorMap teq,
-         const __grid_constant__ CUtensorMap tout, const P p)
+template <int kMode, bool kRev, bool kNorm, bool kPair = false, bool kIdle = false>
+__device__ __forceinline__ void sweep(const CUtensorMap& tfs, const CUtensorMap& tfq, const CUtensorMap& tes,
+                                      const CUtensorMap& teq, const CUtensorMap& tout, const P& p, int block)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // (stays a shared address)
@@ -221,7 +219,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     // this CTA's feature block, segment and sequence
-    int x = blockIdx.x;
+    int x = block;
     const bool second = kPair && x >= p.n0;
     if (second) x -= p.n0;
     const bool rev = kPair ? (second ? p.second.rev : p.rev) != 0 : kRev;
@@ -292,7 +290,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     // state.  384 threads launch with 168 each: 88 + 2 x 208 = 3 x 168; 512 with 128:
     // 96 + 192 + 2 x 112 = 4 x 128 (64 + 192 + 2 x 128 spilled in the loading warps: dphk of
     // B2 H16 L8192 F512 174 against 162 us), or, with half the state and two limbs of scores,
-    // 64 + 128 + 2 x 160.
+    // 64 + 128 + 2 x 160.  A fourth warpgroup that does nothing (kIdle): 24 + 88 + 2 x 200.
     if (warp < 4) {
         regs_dec<kLimb ? 64 : kSplit ? 96 : 88>();
         if (warp == 1 && lane == 0) {
@@ -509,6 +507,8 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
             }
         }
         __syncwarp();
+    } else if (kIdle && warp >= threads(kMode) / 32) {
+        regs_dec<24>();
     } else {
         // ------------------------------------------------------------------ epilogue
         // (no early exit on a wait that ran out: the pairs of warps share named barriers)
@@ -709,7 +709,7 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
             for (int i = 0; i < count; ++i) out_e(i);
             if (lane == 0) bulk_wait<0>();   // this warp's stores have landed
         } else {
-        if (!kLimb) regs_inc<kSplit ? 192 : 208>();
+        if (!kLimb) regs_inc<kSplit ? 192 : kIdle ? 200 : 208>();
         constexpr int kNb = kLimb ? 1 : 2;      // 128-feature blocks
         float run[kNb][kW], zrun[kNb] = {};   // M at (f = 128 b + row, e = 32 half + c); z at b
         auto has_zrow = [&](int b) { return has_z && (kSplit || b == half); };
@@ -1050,6 +1050,33 @@ k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtens
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
+template <int kMode, bool kRev, bool kNorm, bool kPair>
+__global__ void __launch_bounds__(threads(kMode), 1)
+k_tc_dec(const __grid_constant__ CUtensorMap tfs, const __grid_constant__ CUtensorMap tfq,
+         const __grid_constant__ CUtensorMap tes, const __grid_constant__ CUtensorMap teq,
+         const __grid_constant__ CUtensorMap tout, const __grid_constant__ P p)
+{
+    sweep<kMode, kRev, kNorm, kPair>(tfs, tfq, tes, teq, tout, p, blockIdx.x);
+}
+
+// The gradients' sweeps in one launch: dphq (the first n0 CTAs), dphk (the next n1) and, where
+// it has one block of features, dv, whose CTAs leave four warps idle.
+template <bool kNorm>
+__global__ void __launch_bounds__(threads(kOutE), 1)
+k_tc_dec_grads(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+               const __grid_constant__ CUtensorMap tdo, const __grid_constant__ CUtensorMap tq,
+               const __grid_constant__ CUtensorMap tdq, const __grid_constant__ CUtensorMap tdk,
+               const __grid_constant__ P pq, const __grid_constant__ P pk, const __grid_constant__ P pv, int n0, int n1)
+{
+    const int x = blockIdx.x;
+    if (x < n0)
+        sweep<kOutE, false, kNorm>(tk, tk, tv, tdo, tdq, pq, x);
+    else if (x < n0 + n1)
+        sweep<kOutE, true, kNorm>(tq, tq, tdo, tv, tdk, pk, x - n0);
+    else
+        sweep<kOutF, true, kNorm, false, true>(tq, tk, tdo, tdo, tq, pv, x - n0 - n1);
+}
+
 // Segment sums -> the states entering the segments, in place, S (four elements a thread) and z
 // in one launch; first: the state entering the walk (null: zero), last: the one leaving it
 // (null: not wanted; may be first).  Loads run eight segments ahead of the stores (L2 latency
@@ -1346,6 +1373,35 @@ cudaError_t segment_states(const DecayArgs& a, const Carve& k, Start* const* wal
     return e;
 }
 
+template <bool kNorm>
+cudaError_t launch_grads(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dout, const CUtensorMap& q,
+                         const CUtensorMap& dq, const CUtensorMap& dk, const P& pq, const P& pk, const P* pv, int64_t BH,
+                         bool& chained, cudaStream_t st)
+{
+    constexpr size_t smem = std::max(layout(kOutE).total, layout(kOutF).total) + 1024;
+    const auto kernel = k_tc_dec_grads<kNorm>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int n0 = static_cast<int>(BH * pq.nsl * pq.nfb), n1 = static_cast<int>(BH * pk.nsl * pk.nfb);
+    const int n2 = pv ? static_cast<int>(BH * pv->nsl) : 0;
+    const bool first = !chained;
+    chained = true;
+    TraceScope trace_("tc_decay_grads", st);
+    return launch_in_chain(first, +kernel, dim3(static_cast<unsigned>(n0 + n1 + n2)), threads(kOutE), smem, st, k, v, dout, q, dq, dk,
+                           pq, pk, pv ? *pv : pk, n0, n1);
+}
+
+// Whether the gradients' sweeps, of n0, n1 and n2 CTAs, share a launch: sequences of their own
+// lengths even out, so do several waves of CTAs, and few CTAs fill each other's idle SMs.
+// Backward, apart and together: B8 H8 L1111 F128 ragged 69 and 59 us; B32 H12 L1024 F256 383
+// and 351; B1 H4 L1000 F256 41 and 27.  Where each fills most of the GPU once, they had better
+// follow one another: B8 H16 L1000 F128 122 apart, 127 together.
+bool one_launch(const DecayArgs& a, int64_t n0, int64_t n1, int64_t n2)
+{
+    auto waves = [](int64_t n) { return (n + kNumSMs - 1) / kNumSMs; };
+    return a.lengths || std::max(n0, n1) > kNumSMs || waves(n0 + n1 + n2) < waves(n0) + waves(n1) + waves(n2);
+}
+
 // A sweep whose queries are on the F side: one launch per feature block, the blocks'
 // numerators and denominators added in fp32.
 cudaError_t out_f(const CUtensorMap& fs, const CUtensorMap& fq, const CUtensorMap& es, P p, const Plan& c,
@@ -1412,12 +1468,28 @@ cudaError_t decay_tc_bwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
     s.q_mul = rz;
     s.q_off = r;
     s.o = static_cast<__nv_bfloat16*>(a.dphq);
-    if ((e = launch<kOutE>("tc_decay_out_e", mk, mk, mv, mo, mdq, s, cq, false, a.norm, chained, st)) != cudaSuccess) return e;
-    if (!both && (e = segment_states(a, k, walks, 1, chained, st)) != cudaSuccess) return e;
-    P w = g;                 // (the state that the walk leaves is dv's sweep to write)
-    w.last = w.last_z = nullptr;
-    w.o = static_cast<__nv_bfloat16*>(a.dphk);
-    if ((e = launch<kOutE>("tc_decay_out_e", mq, mq, mo, mv, mdk, w, c, true, a.norm, chained, st)) != cudaSuccess) return e;
+    auto params_k = [&] {
+        P w = g;              // (the state that the walk leaves is dv's sweep to write)
+        w.last = w.last_z = nullptr;
+        w.o = static_cast<__nv_bfloat16*>(a.dphk);
+        return w;
+    };
+    // The three sweeps in one launch, once the states are there.  (A state that dv's updates in
+    // place is dphk's to read first.)
+    const bool in_place = c.nseg == 1 && a.dS_in && a.dS_in == a.dS_out;
+    const bool three = c.nfb == 1 && !in_place;
+    if ((both || c.nseg == 1) && one_launch(a, c.BH * cq.nseg * cq.nfb, c.BH * c.nseg * c.nfb, three ? c.BH * c.nseg : 0)) {
+        if (!both && (e = segment_states(a, k, walks, 1, chained, st)) != cudaSuccess) return e;
+        g.z_state = g.last_z != nullptr;
+        g.o = static_cast<__nv_bfloat16*>(a.dv);
+        e = a.norm ? launch_grads<true>(mk, mv, mo, mq, mdq, mdk, s, params_k(), three ? &g : nullptr, c.BH, chained, st)
+                   : launch_grads<false>(mk, mv, mo, mq, mdq, mdk, s, params_k(), three ? &g : nullptr, c.BH, chained, st);
+        if (e != cudaSuccess || three) return e;
+    } else {
+        if ((e = launch<kOutE>("tc_decay_out_e", mk, mk, mv, mo, mdq, s, cq, false, a.norm, chained, st)) != cudaSuccess) return e;
+        if (!both && (e = segment_states(a, k, walks, 1, chained, st)) != cudaSuccess) return e;
+        if ((e = launch<kOutE>("tc_decay_out_e", mq, mq, mo, mv, mdk, params_k(), c, true, a.norm, chained, st)) != cudaSuccess) return e;
+    }
     g.z_state = g.last_z != nullptr;
     g.o = static_cast<__nv_bfloat16*>(a.dv);
     return out_f(mq, mk, mo, g, c, k, true, a.norm, chained, st);

@@ -306,6 +306,40 @@ def test_bwd_state_in_place_and_empty():
             assert torch.equal(a, keep)
 
 
+# The backward's launches: sums of both walks together or not, its sweeps in one launch (with dv
+# or without) or one after the other; a final state's gradient updated in place makes no difference.
+@pytest.mark.parametrize("B,H,L,F,norm,ragged,states,one", [
+    (8, 3, 300, 128, True, True, 1, True), (160, 1, 140, 64, False, True, 0, True), (100, 1, 400, 64, True, False, 0, False),
+    (40, 1, 1100, 256, True, False, 1, False), (2, 3, 520, 400, False, True, 1, True), (1, 2, 700, 512, True, False, 1, True),
+    (1, 18, 1500, 128, False, False, 2, False), (170, 1, 130, 512, False, True, 0, True)])
+def test_backward_launches(B, H, L, F, norm, ragged, states, one):
+    test_backward(B, H, L, F, "bf16", norm, ragged, True)
+    c, g = _case(B, H, L, F, "bf16", norm, ragged, True, seed=4)
+    out, den, _, _ = _forward(c, "bf16")
+    c["dout"] = _randn(g, B, H, L, 64).bfloat16()
+    if norm:
+        c["out"], c["den"] = out, den
+    dS, dz = _randn(g, B, H, F, 64), _randn(g, B, H, F) if norm else None
+
+    def run(in_place):
+        grads = {k: torch.full_like(c[x], MARK) for k, x in (("dphq", "phq"), ("dphk", "phk"), ("dv", "v"))}
+        dS_out, dz_out = dS.clone(), dz.clone() if norm else None
+        dS_in, dz_in = (dS_out, dz_out) if in_place else (torch.empty_like(dS), torch.empty_like(dz) if norm else None)
+        bd.slay_decay_attn_bwd(**c, **grads, dS_out=dS_out, dz_out=dz_out, dS_in=dS_in, dz_in=dz_in)
+        return [x for x in (*grads.values(), dS_in, dz_in) if x is not None]
+
+    bd.slay_trace_enable(True)
+    try:
+        bd.slay_trace_read()
+        apart = run(False)
+        torch.cuda.synchronize()
+        names = [n for n, _ in bd.slay_trace_read()]
+    finally:
+        bd.slay_trace_enable(False)
+    assert names.count("tc_decay_state") == states and ("tc_decay_grads" in names) == one, names
+    assert all(torch.equal(x, y) for x, y in zip(apart, run(True)))
+
+
 def test_runs_are_bit_identical():
     c, g = _case(2, 3, 1000, 256, "bf16", True, True, True, kind="slow")
     a, b = _forward(c, "bf16"), _forward(c, "bf16")
