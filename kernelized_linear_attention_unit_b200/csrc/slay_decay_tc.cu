@@ -1476,7 +1476,7 @@ cudaError_t decay_tc_bwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
     };
     // The three sweeps in one launch, once the states are there.  (A state that dv's updates in
     // place is dphk's to read first.)
-    const bool in_place = c.nseg == 1 && a.dS_in && a.dS_in == a.dS_out;
+    const bool in_place = c.nseg == 1 && ((a.dS_in && a.dS_in == a.dS_out) || (a.dz_in && a.dz_in == a.dz_out));
     const bool three = c.nfb == 1 && !in_place;
     if ((both || c.nseg == 1) && one_launch(a, c.BH * cq.nseg * cq.nfb, c.BH * c.nseg * c.nfb, three ? c.BH * c.nseg : 0)) {
         if (!both && (e = segment_states(a, k, walks, 1, chained, st)) != cudaSuccess) return e;
