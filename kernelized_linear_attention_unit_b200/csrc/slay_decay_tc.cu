@@ -1148,7 +1148,7 @@ bool map_rows(CUtensorMap* m, const void* base, int cols, int L, int64_t BH, boo
               out ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a sweep is cut: blocks of at most `most` features, and as many segments of the sequence
+// How a sweep is cut: blocks of at most `block` features, and as many segments of the sequence
 // as give each CTA an SM.  More of them cost more than they balance: forward B4 H8 L2048 F256
 // 40 us with four, 54 with eight; backward B2 H16 L8192 F512 657 with four, 694 with nine
 // (1.95 waves instead of 0.86); ragged batches too, forward B8 H16 L1500 F128 43 with one, 56
@@ -1158,15 +1158,27 @@ struct Plan {
     int64_t BH;
 };
 
-Plan plan(const DecayArgs& a, int most, bool blocks_in_grid)
+int chunks(const DecayArgs& a) { return (a.L + kT - 1) / kT; }
+int64_t waves(int64_t ctas) { return (ctas + kNumSMs - 1) / kNumSMs; }
+
+Plan plan(const DecayArgs& a, int block, bool blocks_in_grid)
 {
     Plan c{};
     c.BH = static_cast<int64_t>(a.B) * a.H;
-    c.nfb = (a.F + most - 1) / most;
+    c.nfb = (a.F + block - 1) / block;
     c.fw = ((a.F + c.nfb - 1) / c.nfb + 63) & ~63;
     const int64_t units = c.BH * (blocks_in_grid ? c.nfb : 1);
-    const int nch = (a.L + kT - 1) / kT;
-    c.nseg = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kNumSMs / units, nch)));
+    const int nch = chunks(a);
+    const int most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kNumSMs / units, nch)));
+    // the fewest segments of the shortest time: a walk's chunks, and one and a half more for the
+    // states that segments need first
+    int best = 2 * nch;
+    c.nseg = 1;
+    for (int n = 2; n <= most; ++n)
+        if (2 * ((nch + n - 1) / n) + 3 < best) {
+            best = 2 * ((nch + n - 1) / n) + 3;
+            c.nseg = n;
+        }
     return c;
 }
 
@@ -1180,6 +1192,42 @@ Plan plan_q(const DecayArgs& a)
     const Plan h = plan(a, kMaxFw / 2, true);
     if (a.norm || (h.nseg == 1 && h.BH * h.nfb <= kNumSMs)) return h;
     return plan(a, kMaxFw, true);
+}
+
+// The backward's: its three sweeps side by side fill the GPU with a third of the segments, often
+// without any.  Compared in half chunks of a CTA (launches and states included): that, with the
+// same segments for both walks, whose sums share a launch, and one sweep after the other, each
+// cut for itself.  The latter and the former, measured: B2 H16 L2048 F256 115 and 80 us, B4 H12
+// L1024 F64 normalized 63 and 39, B8 H8 L1111 F128 ragged 59 and 49; but B1 H16 L4096 F128 76
+// and 85.
+struct BwdPlan {
+    Plan k, q;   // dphk and dv, dphq
+};
+
+BwdPlan plan_bwd(const DecayArgs& a)
+{
+    BwdPlan b{plan_f(a), plan_q(a)};
+    const int64_t BH = b.k.BH, cs = plan(a, kMaxFw, true).nfb;
+    const int nch = chunks(a);
+    auto len = [&](int n) { return static_cast<int64_t>((nch + n - 1) / n); };
+    auto sums = [&](int n) { return n > 1 ? 3 + waves(BH * cs * n) * len(n) : 0; };
+    int64_t best = 4 * (2 * (waves(BH * b.q.nfb * b.q.nseg) * len(b.q.nseg) +
+                             (waves(BH * b.k.nfb * b.k.nseg) + b.k.nfb * waves(BH * b.k.nseg)) * len(b.k.nseg)) +
+                        4 + sums(b.q.nseg) + sums(b.k.nseg));
+    const int most = static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, kNumSMs / (2 * BH * cs)), nch));
+    int joined = 0;
+    for (int n = 1; n <= most; ++n) {
+        // (with a second block of dv's features it has to be clearly shorter)
+        const int64_t t = (b.k.nfb > 1 ? 5 : 4) *
+                          (2 * (waves(BH * (b.q.nfb + b.k.nfb + 1) * n) + (b.k.nfb - 1) * waves(BH * n)) * len(n) +
+                           (n > 1 ? 3 + 2 * len(n) : 0));
+        if (joined ? t < best : t <= best) {
+            best = t;
+            joined = n;
+        }
+    }
+    if (joined) b.k.nseg = b.q.nseg = joined;
+    return b;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1215,8 +1263,16 @@ Carve carve(const DecayArgs& a, bool bwd, void* ws)
         }
         return s;
     };
-    k.walk = segs(c.nseg);
-    if (c.nseg > 1) {
+    int nseg = c.nseg, nseg_q = 1;
+    if (bwd) {                  // (the size of a workspace serves either form)
+        DecayArgs other = a;
+        other.norm = !a.norm;
+        const BwdPlan x = plan_bwd(a), y = plan_bwd(other);
+        nseg = std::max(x.k.nseg, y.k.nseg);
+        nseg_q = std::max(x.q.nseg, y.q.nseg);
+    }
+    k.walk = segs(nseg);
+    if (nseg > 1) {
         k.in = take(static_cast<size_t>(c.BH) * a.F * 64);
         k.in_z = take(static_cast<size_t>(c.BH) * a.F);
     }
@@ -1228,9 +1284,7 @@ Carve carve(const DecayArgs& a, bool bwd, void* ws)
     if (bwd) {
         k.rz = take(rows);
         k.r = take(rows);
-        DecayArgs other = a;    // (the size of a workspace serves either form)
-        other.norm = !a.norm;
-        k.walk_q = segs(std::max(plan_q(a).nseg, plan_q(other).nseg));
+        k.walk_q = segs(nseg_q);
     }
     k.bytes = o;
     return k;
@@ -1296,7 +1350,7 @@ struct Start {
     bool rev;
     const float *first, *first_z;
     float *last, *last_z;
-    bool scan() const { return c->nseg > kMaxSums; }
+    bool scan() const { return c->nseg - 1 + (first ? 2 : 0) > kMaxSums - 1; }
     int summed() const { return scan() ? c->nseg : c->nseg - 1; }   // (without a scan nobody adds the last segment's)
 };
 
@@ -1398,7 +1452,6 @@ cudaError_t launch_grads(const CUtensorMap& k, const CUtensorMap& v, const CUten
 // follow one another: B8 H16 L1000 F128 122 apart, 127 together.
 bool one_launch(const DecayArgs& a, int64_t n0, int64_t n1, int64_t n2)
 {
-    auto waves = [](int64_t n) { return (n + kNumSMs - 1) / kNumSMs; };
     return a.lengths || std::max(n0, n1) > kNumSMs || waves(n0 + n1 + n2) < waves(n0) + waves(n1) + waves(n2);
 }
 
@@ -1446,7 +1499,8 @@ cudaError_t decay_tc_fwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
 
 cudaError_t decay_tc_bwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st)
 {
-    const Plan c = plan_f(a), cq = plan_q(a);
+    const BwdPlan b = plan_bwd(a);
+    const Plan &c = b.k, &cq = b.q;
     const Carve k = carve(a, true, ws);
     CUtensorMap mq, mk, mv, mo, mdq, mdk;
     if (!map_rows(&mq, a.phq, a.F, a.L, c.BH) || !map_rows(&mk, a.phk, a.F, a.L, c.BH) ||

@@ -309,9 +309,10 @@ def test_bwd_state_in_place_and_empty():
 # The backward's launches: sums of both walks together or not, its sweeps in one launch (with dv
 # or without) or one after the other; a final state's gradient updated in place makes no difference.
 @pytest.mark.parametrize("B,H,L,F,norm,ragged,states,one", [
-    (8, 3, 300, 128, True, True, 1, True), (160, 1, 140, 64, False, True, 0, True), (100, 1, 400, 64, True, False, 0, False),
-    (40, 1, 1100, 256, True, False, 1, False), (2, 3, 520, 400, False, True, 1, True), (1, 2, 700, 512, True, False, 1, True),
-    (1, 18, 1500, 128, False, False, 2, False), (170, 1, 130, 512, False, True, 0, True)])
+    (8, 3, 300, 128, True, True, 0, True), (160, 1, 140, 64, False, True, 0, True), (100, 1, 400, 64, True, False, 0, False),
+    (40, 1, 1100, 256, True, False, 0, True), (2, 3, 520, 400, False, True, 1, True), (1, 2, 700, 512, True, False, 1, True),
+    (1, 18, 4500, 128, False, False, 2, False), (170, 1, 130, 512, False, True, 0, True), (1, 4, 900, 256, True, False, 1, True),
+    (2, 9, 1800, 320, True, False, 2, False), (32, 1, 1100, 512, True, False, 1, False)])
 def test_backward_launches(B, H, L, F, norm, ragged, states, one):
     test_backward(B, H, L, F, "bf16", norm, ragged, True)
     c, g = _case(B, H, L, F, "bf16", norm, ragged, True, seed=4)
