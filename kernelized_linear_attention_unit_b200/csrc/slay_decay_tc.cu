@@ -1148,11 +1148,12 @@ bool map_rows(CUtensorMap* m, const void* base, int cols, int L, int64_t BH, boo
               out ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a sweep is cut: blocks of at most `block` features, and as many segments of the sequence
-// as give each CTA an SM.  More of them cost more than they balance: forward B4 H8 L2048 F256
-// 40 us with four, 54 with eight; backward B2 H16 L8192 F512 657 with four, 694 with nine
-// (1.95 waves instead of 0.86); ragged batches too, forward B8 H16 L1500 F128 43 with one, 56
-// with two, backward B8 H8 L1111 F128 76 with two, 82 with three.
+// How a sweep is cut: blocks of at most `block` features, and segments of the sequence, as many
+// as shorten it while each CTA finds an SM.  More of them cost more than they balance: forward
+// B4 H8 L2048 F256 40 us with four, 54 with eight; backward B2 H16 L8192 F512 657 with four, 694
+// with nine (1.95 waves instead of 0.86); ragged batches too, forward B8 H16 L1500 F128 43 with
+// one, 56 with two.  Short sequences stay whole: forward B3 H24 L384 F128 16 us with one, 18.6
+// with two; B3 H24 L640 F256 (two) 34, with one 35.
 struct Plan {
     int nfb, fw, nseg;
     int64_t BH;
@@ -1336,9 +1337,10 @@ P base(const DecayArgs& a, const Plan& c, int* err)
 
 // What the output sweeps start from, and the state that the walk leaves.  Up to kMaxSums
 // segments, each sweep adds up the sums of the segments before its own (66 KB each from L2, at
-// F = 256) and the one that walks last writes the state; beyond, a scan kernel does both.
-// Forward at F = 256: four segments (B4 H8 L2048) 40 us against 44 with the scan, nine
-// (B1 H16 L16384) 128 against 118.
+// F = 256) and the one that walks last writes the state; beyond, a scan kernel does both.  A
+// state that enters the walk counts as two more.  Forward at F = 256: four segments (B4 H8 L2048)
+// 40 us against 44 with the scan, nine (B1 H16 L16384) 128 against 118, three and a carried
+// state (B1 H4 L384) 22.6 against 18.5, two and one (B3 H24 L384) 28 against 31.
 constexpr int kMaxSums = 4;
 
 // A walk whose segments' states are wanted.
@@ -1354,8 +1356,8 @@ struct Start {
     int summed() const { return scan() ? c->nseg : c->nseg - 1; }   // (without a scan nobody adds the last segment's)
 };
 
-// Two walks' sums come from one launch where its CTAs still find an SM each: backward B8 H8
-// L1111 F128 69 us, 76 one after the other; beyond, the sweep that follows a walk's own launch
+// Two walks' sums come from one launch where its CTAs still find an SM each: backward B1 H4
+// L1000 F256 41 us, 47 one after the other; beyond, the sweep that follows a walk's own launch
 // finds its rows in L2, B1 H8 L16000 F256 170 us against 181.
 bool together(const DecayArgs& a, const Start& x, const Start& y)
 {
@@ -1447,8 +1449,8 @@ cudaError_t launch_grads(const CUtensorMap& k, const CUtensorMap& v, const CUten
 
 // Whether the gradients' sweeps, of n0, n1 and n2 CTAs, share a launch: sequences of their own
 // lengths even out, so do several waves of CTAs, and few CTAs fill each other's idle SMs.
-// Backward, apart and together: B8 H8 L1111 F128 ragged 69 and 59 us; B32 H12 L1024 F256 383
-// and 351; B1 H4 L1000 F256 41 and 27.  Where each fills most of the GPU once, they had better
+// Backward, apart and together: B8 H8 L1111 F128 ragged (in two segments) 69 and 59 us; B32 H12
+// L1024 F256 383 and 351; B1 H4 L1000 F256 41 and 27.  Where each fills most of the GPU once, they had better
 // follow one another: B8 H16 L1000 F128 122 apart, 127 together.
 bool one_launch(const DecayArgs& a, int64_t n0, int64_t n1, int64_t n2)
 {
