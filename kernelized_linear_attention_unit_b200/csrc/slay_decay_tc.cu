@@ -1173,13 +1173,8 @@ Plan plan(const DecayArgs& a, int block, bool blocks_in_grid)
     const int most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kNumSMs / units, nch)));
     // the fewest segments of the shortest time: a walk's chunks, and one and a half more for the
     // states that segments need first
-    int best = 2 * nch;
-    c.nseg = 1;
-    for (int n = 2; n <= most; ++n)
-        if (2 * ((nch + n - 1) / n) + 3 < best) {
-            best = 2 * ((nch + n - 1) / n) + 3;
-            c.nseg = n;
-        }
+    const int len = (nch + most - 1) / most;
+    c.nseg = 2 * len + 3 < 2 * nch ? (nch + len - 1) / len : 1;
     return c;
 }
 
@@ -1217,7 +1212,8 @@ BwdPlan plan_bwd(const DecayArgs& a)
                         4 + sums(b.q.nseg) + sums(b.k.nseg));
     const int most = static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, kNumSMs / (2 * BH * cs)), nch));
     int joined = 0;
-    for (int n = 1; n <= most; ++n) {
+    // (of the numbers of segments that give the same length, the least)
+    for (int n = 1; n <= most; n = len(n) > 1 ? (nch + static_cast<int>(len(n)) - 2) / (static_cast<int>(len(n)) - 1) : most + 1) {
         // (with a second block of dv's features it has to be clearly shorter)
         const int64_t t = (b.k.nfb > 1 ? 5 : 4) *
                           (2 * (waves(BH * (b.q.nfb + b.k.nfb + 1) * n) + (b.k.nfb - 1) * waves(BH * n)) * len(n) +
