@@ -179,10 +179,16 @@ def slay_path(op, dtype, B, H, L, D, Dv, R, m) -> int:
     return n
 
 
-def alloc_workspace(op, dtype, B, H, L, D, Dv, R, m, device=None):
+def alloc_workspace(op, dtype, B, H, L, D, Dv, R, m, device=None, stream=None):
     """Caller-owned workspace of the size the library asks for (torch allocation).  When the
     call needs none (empty work, which enqueues nothing and leaves the workspace as it is),
-    a zeroed 256-byte block, so that slay_kernel_status on it reads a clear status word."""
+    a zeroed 256-byte block, so that slay_kernel_status on it reads a clear status word.
+    stream: the one the call will run on (None: the current one).  The block comes from that
+    stream's memory: torch hands out blocks whose last kernels are still queued on the stream
+    they were allocated for, and only work on the same stream runs behind those."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return alloc_workspace(op, dtype, B, H, L, D, Dv, R, m, device)
     n = slay_workspace_bytes(op, dtype, B, H, L, D, Dv, R, m)
     if n == 0:
         return torch.zeros(256, dtype=torch.uint8, device=device or "cuda")
@@ -242,7 +248,7 @@ def _attn(fn, name, op, q, k, v, out, den, R, m, seed, eps, workspace, stream):
     dt = _dt(q)
     need = slay_workspace_bytes(op, dt, B, H, L, D, Dv, R, m)
     if workspace is None:
-        workspace = alloc_workspace(op, dt, B, H, L, D, Dv, R, m, q.device)
+        workspace = alloc_workspace(op, dt, B, H, L, D, Dv, R, m, q.device, stream)
     _check(workspace, "workspace")
     wbytes = workspace.numel() * workspace.element_size()
     if wbytes < need:
@@ -295,7 +301,7 @@ def _attn_bwd(fn, name, op, q, k, v, out, den, dout, dq, dk, dv, R, m, seed, eps
     dt = _dt(q)
     need = slay_workspace_bytes(op, dt, B, H, L, D, Dv, R, m)
     if workspace is None:
-        workspace = alloc_workspace(op, dt, B, H, L, D, Dv, R, m, q.device)
+        workspace = alloc_workspace(op, dt, B, H, L, D, Dv, R, m, q.device, stream)
     wbytes = workspace.numel() * workspace.element_size()
     if wbytes < need:
         raise ValueError("workspace has %d bytes, %d needed" % (wbytes, need))
@@ -359,7 +365,7 @@ def slay_linear_attn_fwd(phq, phk, v, out, den, eps, causal, workspace=None, str
         _check(den, "den", torch.float32, (B, H, L))
     dt = _dt(phq)
     if workspace is None:
-        workspace = alloc_workspace(OP_LINEAR_ATTN, dt, B, H, L, 64, Dv, 1, F, phq.device)
+        workspace = alloc_workspace(OP_LINEAR_ATTN, dt, B, H, L, 64, Dv, 1, F, phq.device, stream)
     wbytes = workspace.numel() * workspace.element_size()
     _raise(lib().slay_linear_attn_fwd(_ptr(phq), _ptr(phk), _ptr(v), _ptr(out), _ptr(den), B, H,
                                       L, F, Dv, dt, eps, 1 if causal else 0, _ptr(workspace),
@@ -392,7 +398,7 @@ def slay_attn_causal_fwd_state(q, k, v, out, den, R, m, seed, eps, S_in=None, z_
     so, zo = _state_ptrs(S_out, z_out, (B, H), F, "state out")
     dt = _dt(q)
     if workspace is None:
-        workspace = alloc_workspace(OP_CAUSAL_FWD, dt, B, H, L, D, Dv, R, m, q.device)
+        workspace = alloc_workspace(OP_CAUSAL_FWD, dt, B, H, L, D, Dv, R, m, q.device, stream)
     wbytes = workspace.numel() * workspace.element_size()
     _raise(lib().slay_attn_causal_fwd_state(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(den), si, zi,
                                             so, zo, B, H, L, D, Dv, dt, R, m, seed, eps,
@@ -413,7 +419,7 @@ def slay_causal_state(k, v, S_out, z_out, R, m, seed, eps, S_in=None, z_in=None,
     so, zo = _state_ptrs(S_out, z_out, (B, H), F, "state out")
     dt = _dt(k)
     if workspace is None:
-        workspace = alloc_workspace(OP_CAUSAL_STATE, dt, B, H, L, D, Dv, R, m, k.device)
+        workspace = alloc_workspace(OP_CAUSAL_STATE, dt, B, H, L, D, Dv, R, m, k.device, stream)
     wbytes = workspace.numel() * workspace.element_size()
     _raise(lib().slay_causal_state(_ptr(k), _ptr(v), si, zi, so, zo, B, H, L, D, Dv, dt, R, m,
                                    seed, eps, _ptr(workspace), wbytes, _stream(stream)),
@@ -434,7 +440,7 @@ def slay_attn_causal_fwd_begin(k, v, S_out, z_out, R, m, seed, eps, workspace=No
     so, zo = _state_ptrs(S_out, z_out, (B, H), F, "state out")
     dt = _dt(k)
     if workspace is None:
-        workspace = alloc_workspace(OP_CAUSAL_FWD_SPLIT, dt, B, H, L, D, Dv, R, m, k.device)
+        workspace = alloc_workspace(OP_CAUSAL_FWD_SPLIT, dt, B, H, L, D, Dv, R, m, k.device, stream)
     wbytes = workspace.numel() * workspace.element_size()
     _raise(lib().slay_attn_causal_fwd_begin(_ptr(k), _ptr(v), so, zo, B, H, L, D, Dv, dt, R, m,
                                             seed, eps, _ptr(workspace), wbytes, _stream(stream)),
@@ -520,7 +526,7 @@ def _bwd_piece(fn, name, q, k, v, out, den, dout, dq, dk, dv, R, m, seed, eps, S
     gi, zgi = _state_ptrs(G_in, zg_in, (B, H), F, "state after")
     dt = _dt(q)
     if workspace is None:
-        workspace = alloc_workspace(OP_CAUSAL_BWD, dt, B, H, L, D, Dv, R, m, q.device)
+        workspace = alloc_workspace(OP_CAUSAL_BWD, dt, B, H, L, D, Dv, R, m, q.device, stream)
     wbytes = workspace.numel() * workspace.element_size()
     _raise(fn(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(den), _ptr(dout), _ptr(dq), _ptr(dk),
               _ptr(dv), si, zi, gi, zgi, B, H, L, D, Dv, dt, R, m, seed, eps, _ptr(workspace),
@@ -554,7 +560,7 @@ def _g_state(fn, name, q, out, den, dout, G_out, zg_out, R, m, seed, eps, worksp
     go, zgo = _state_ptrs(G_out, zg_out, (B, H), F, "state out")
     dt = _dt(q)
     if workspace is None:
-        workspace = alloc_workspace(OP_CAUSAL_BWD, dt, B, H, L, D, Dv, R, m, q.device)
+        workspace = alloc_workspace(OP_CAUSAL_BWD, dt, B, H, L, D, Dv, R, m, q.device, stream)
     wbytes = workspace.numel() * workspace.element_size()
     _raise(fn(_ptr(q), _ptr(out), _ptr(den), _ptr(dout), go, zgo, B, H, L, D, Dv, dt, R, m, seed,
               eps, _ptr(workspace), wbytes, _stream(stream)), name)
@@ -653,9 +659,7 @@ def _decay_common(phq, phk, v, log_decay, lengths):
 
 def _decay_workspace(op, dt, B, H, L, F, Dv, workspace, dev, stream):
     if workspace is None:
-        workspace = alloc_workspace(op, dt, B, H, L, 64, Dv, 1, F, dev)
-        if stream is not None:   # allocated on the current stream, used on the caller's
-            workspace.record_stream(stream)
+        workspace = alloc_workspace(op, dt, B, H, L, 64, Dv, 1, F, dev, stream)
     _check_on(dev, workspace, "workspace")
     return workspace, workspace.numel() * workspace.element_size()
 
