@@ -490,8 +490,9 @@ slay_status slay_attn_causal_fwd_noalloc(const void* q, const void* k, const voi
  * NULL, of the last slay_attn_causal_fwd_noalloc call and the last slay_feature_map call
  * on the current device: the library's own status words).
  * The tensor-core kernels coordinate their warps through shared-memory barriers; every
- * wait is bounded (2 s).  A wait that runs out makes the kernel stop early, leave its
- * outputs incomplete and set the status word, the first int of the workspace, which each
+ * wait is bounded (2 s).  A wait that runs out makes the kernel stop early (the decayed
+ * sweeps: go on without waiting), leave its outputs incomplete, and undefined where they
+ * were written, and set the status word, the first int of the workspace, which each
  * attention call clears when it is enqueued.  This call copies the word to the host on
  * `stream` and synchronizes the stream.  Returns SLAY_ERR_TIMEOUT if the word is set,
  * SLAY_OK if it is not (or if neither of those paths ran on this device),
@@ -500,14 +501,16 @@ slay_status slay_attn_causal_fwd_noalloc(const void* q, const void* k, const voi
 slay_status slay_kernel_status(const void* workspace, void* stream);
 
 /* Test hook for the failure path of the bounded waits (the pages have no counterpart;
- * off by default, for tests only).  With on != 0, the next slay_feature_map call that runs
+ * off by default, for tests only).  With on == 1, the next slay_feature_map call that runs
  * the tensor-core kernel bounds every wait of that launch at 1 ms and has one warp
  * withhold one release of a projection buffer (a barrier that guards no copy or MMA in
  * flight), so that the issuing thread waits for a phase that never completes: the wait
  * runs out, the kernel stops early (its phi output is then incomplete), drains, frees its
  * tensor memory and sets the feature-map status word, which slay_kernel_status(NULL, ...)
- * reports as SLAY_ERR_TIMEOUT.  The hook disarms itself at that launch; on == 0 disarms
- * it earlier.  No GPU fault is involved and the context stays usable.  Returns SLAY_OK. */
+ * reports as SLAY_ERR_TIMEOUT.  With on == 2, in the next slay_decay_attn_fwd or
+ * slay_decay_attn_bwd call that runs on tensor cores, the first CTA of each sweep issues none
+ * of its loads: the waits for them run out after their 2 s, and the workspace's status word
+ * is set.  The hook disarms itself at that call; on == 0 disarms it earlier.  No GPU fault is involved and the context stays usable.  Returns SLAY_OK. */
 slay_status slay_debug_expire_wait(int on);
 
 /* Workspace bytes an entry point needs for these sizes (0 if none; SIZE_MAX if the

@@ -875,7 +875,8 @@ slay_status slay_sketch_params(int D, int R, int m, uint64_t seed, float eps, fl
 
 slay_status slay_debug_expire_wait(int on)
 {
-    fmap_arm_wait_fault(on);
+    fmap_arm_wait_fault(on != 2 ? on : 0);
+    decay_arm_wait_fault(on == 2);
     return SLAY_OK;
 }
 

@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "slay_decay.h"
@@ -145,6 +146,7 @@ struct P {
         int rev, nseg, seg0, nsl;
     } second;
     int* err;
+    int withhold;                                 // test hook, 0 in every normal call: see slay_debug_expire_wait
 };
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -168,8 +170,9 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t x)
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(x) : "memory");
 }
 
-// A wait on the completion of `phase`, bounded by a number of tries (each suspends the thread
-// for a time that the hardware chooses): between about 0.05 s and a few seconds.
+// A wait on the completion of `phase`, bounded in time (kWaitNs; the low word of the clock turns
+// over after 4.3 s).  The clock is read only once a first try, which suspends the thread for a
+// while, has come back empty; after a wait that ran out, each further one is a single try.
 struct Bounded {
     bool ok = true;
     uint32_t where = 0;
@@ -177,10 +180,20 @@ struct Bounded {
     {
         const uint32_t addr = smem_u32(bar);
         if (mbar_try_wait(addr, phase)) return;
-        for (int it = ok ? 1 << 22 : 1; it > 0; --it)
-            if (mbar_try_wait(addr, phase)) return;
-        if (ok) where = 0x10000u | (addr & 0xFFFFu);
+        if (ok) {
+            const uint32_t t0 = clock_ns();
+            do {
+                if (mbar_try_wait(addr, phase)) return;
+            } while (clock_ns() - t0 <= static_cast<uint32_t>(kWaitNs));
+            where = 0x10000u | (addr & 0xFFFFu);
+        }
         ok = false;
+    }
+    static __device__ __forceinline__ uint32_t clock_ns()
+    {
+        uint32_t t;
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+        return t;
     }
     __device__ __forceinline__ void report(int* status) const
     {
@@ -295,7 +308,8 @@ __device__ __forceinline__ void sweep(const CUtensorMap& tfs, const CUtensorMap&
         regs_dec<kLimb ? 64 : kSplit ? 96 : 88>();
         if (warp == 1 && lane == 0) {
             // -------------------------------------------------------------- TMA loads
-            for (int i = 0; i < count && wt.ok; ++i) {
+            // (under the test hook the first CTA loads nothing)
+            for (int i = p.withhold && block == 0 ? count : 0; i < count && wt.ok; ++i) {
                 const int t0 = chunk_of(i) * kT, b = i % kEs;
                 auto load_e = [&] {   // the 64-wide rows
                     if (i >= kEs) wait_k(B_ESE + b, i / kEs - 1);
@@ -349,7 +363,8 @@ __device__ __forceinline__ void sweep(const CUtensorMap& tfs, const CUtensorMap&
                 tc_fence_after();
             };
             int fq = 0, fqr = 0;   // query slot, its use
-            for (int i = 0; i < count && wt.ok; ++i) {
+            for (int i = 0; i < count; ++i) {
+                if (!__all_sync(0xffffffffu, wt.ok)) break;   // the warp leaves as one: elect_one needs all of it
                 const int t0 = chunk_of(i) * kT, n = min(kT, len - t0), eb = i % kEs;
                 // rows of the tensor behind this sequence may hold anything: cleared in the
                 // tiles, since they enter sums over tokens (rows past L arrive as zero)
@@ -1315,9 +1330,13 @@ cudaError_t launch(const char* name, const CUtensorMap& fs, const CUtensorMap& f
     return norm ? launch1<kMode, false, true>(fs, fq, es, eq, out, p, c, chained, st) : launch1<kMode, false, false>(fs, fq, es, eq, out, p, c, chained, st);
 }
 
-P base(const DecayArgs& a, const Plan& c, int* err)
+// Armed by slay_debug_expire_wait(2), consumed by the next call that runs these sweeps.
+std::atomic<int> g_wait_fault{0};
+
+P base(const DecayArgs& a, const Plan& c, int* err, bool withhold)
 {
     P p{};
+    p.withhold = withhold;
     p.log_decay = a.log_decay;
     p.lengths = a.lengths;
     p.H = a.H;
@@ -1471,6 +1490,8 @@ cudaError_t out_f(const CUtensorMap& fs, const CUtensorMap& fq, const CUtensorMa
 
 }  // namespace
 
+void decay_arm_wait_fault(bool on) { g_wait_fault.store(on ? 1 : 0); }
+
 bool decay_tc_supported(const DecayArgs& a)
 {
     return a.dt == SLAY_BF16 && a.L > 0 && a.F % 8 == 0 && a.F <= 2 * kMaxFw;
@@ -1485,7 +1506,7 @@ cudaError_t decay_tc_fwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
     CUtensorMap mq, mk, mv;
     if (!map_rows(&mq, a.phq, a.F, a.L, c.BH) || !map_rows(&mk, a.phk, a.F, a.L, c.BH) || !map_rows(&mv, a.v, 64, a.L, c.BH))
         return cudaErrorInvalidValue;
-    P p = base(a, c, err);
+    P p = base(a, c, err, g_wait_fault.exchange(0) != 0);
     bool chained = false;   // whether a kernel of this call runs before
     Start w{&c, k.walk, &p, &mk, &mv, false, a.S_in, a.z_in, a.S_out, a.z_out}, *walks[] = {&w};
     cudaError_t e = segment_states(a, k, walks, 1, chained, st);
@@ -1509,8 +1530,9 @@ cudaError_t decay_tc_bwd(const DecayArgs& a, void* ws, int* err, cudaStream_t st
     cudaError_t e = a.norm ? decay_row_stats(a, k.rz, k.r, st) : cudaSuccess;
     if (e != cudaSuccess) return e;
     const float *rz = a.norm ? k.rz : nullptr, *r = a.norm ? k.r : nullptr;
-    P s = base(a, cq, err);   // dphq from the states before each token
-    P g = base(a, c, err);    // dphk and dv from the states after each token
+    const bool withhold = g_wait_fault.exchange(0) != 0;
+    P s = base(a, cq, err, withhold);   // dphq from the states before each token
+    P g = base(a, c, err, withhold);    // dphk and dv from the states after each token
     g.s_mul = rz;
     g.s_off = r;
     Start before{&cq, k.walk_q, &s, &mk, &mv, false, a.S_in, a.z_in, nullptr, nullptr};

@@ -88,6 +88,8 @@ const void* noalloc_status_word();
 // Workspace bytes and slay_path mask of the decayed forward and backward (slay_decay_api.cu).
 size_t decay_ws(slay_op op, slay_dtype dt, int B, int H, int L, int F);
 int decay_path(slay_op op, slay_dtype dt, int B, int H, int L, int F);
+// Test hook: the next decayed forward or backward on tensor cores runs into its bounded waits.
+void decay_arm_wait_fault(bool on);
 
 // ---- CUDA-core kernels (slay_simt.cu) ----
 // Sizes of the workspace carve-outs of the CUDA-core path.
