@@ -25,15 +25,18 @@ bool pair_ok(const float* S, const float* z, bool norm)
     return norm ? z && aligned(z, 16) : !z;
 }
 
+// grid limits of the launches: (b, h), up to three times, indexes grid y / z
+bool grid_ok(int B, int H, int L)
+{
+    return static_cast<int64_t>(B) * H <= 65535 / 3 && (static_cast<int64_t>(L) + 63) / 64 <= 65535;
+}
+
 slay_status check_sizes(int B, int H, int L, int F, int Dv, slay_dtype dt, bool norm, float eps)
 {
     if (B < 0 || H < 0 || L < 0 || F <= 0 || Dv <= 0) return SLAY_ERR_INVALID_ARG;
     if (Dv != kD || F > kMaxF) return SLAY_ERR_UNSUPPORTED;
     if (!dtype_ok(dt) || (norm && !eps_ok(eps))) return SLAY_ERR_INVALID_ARG;
-    // grid limits of the launches: (b, h), up to three times, indexes grid y / z
-    if (static_cast<int64_t>(B) * H > 65535 / 3 || (static_cast<int64_t>(L) + 63) / 64 > 65535)
-        return SLAY_ERR_UNSUPPORTED;
-    return SLAY_OK;
+    return grid_ok(B, H, L) ? SLAY_OK : SLAY_ERR_UNSUPPORTED;
 }
 
 DecayArgs sizes(int B, int H, int L, int F, slay_dtype dt, bool norm)
@@ -52,6 +55,7 @@ DecayArgs sizes(int B, int H, int L, int F, slay_dtype dt, bool norm)
 
 size_t decay_ws(slay_op op, slay_dtype dt, int B, int H, int L, int F)
 {
+    if (!grid_ok(B, H, L)) return SIZE_MAX;
     if (static_cast<int64_t>(B) * H * L == 0) return 0;
     const DecayArgs a = sizes(B, H, L, F, dt, true);
     const bool bwd = op == SLAY_OP_DECAY_BWD;
@@ -60,6 +64,7 @@ size_t decay_ws(slay_op op, slay_dtype dt, int B, int H, int L, int F)
 
 int decay_path(slay_op, slay_dtype dt, int B, int H, int L, int F)
 {
+    if (!grid_ok(B, H, L)) return -1;
     return static_cast<int64_t>(B) * H > 0 && decay_tc_supported(sizes(B, H, L, F, dt, true)) ? SLAY_PATH_TC_CONTRACTION : 0;
 }
 
