@@ -365,7 +365,7 @@ slay_status slay_linear_attn_fwd(const void* phq, const void* phk, const void* v
  * workspace : slay_workspace_bytes(SLAY_OP_DECAY_FWD, dt, B, H, L, 64, Dv, 1, F) bytes; it
  *             serves one call at a time, captured graphs that hold it included.
  * Outputs share no memory with inputs, but that S_out, z_out may be S_in, z_in.  A token of a sequence that is not
- * finite may reach every row of its 128-token chunk.  B*H <= 21845.
+ * finite may reach every row of its 128-token chunk.  B*H <= 21845, L <= 4194240.
  * bf16 with F % 8 == 0, F <= 512 runs on tensor cores (SLAY_PATH_TC_CONTRACTION): fp32
  * accumulation; the masked scores and the state's operand are rounded to bf16, den and the
  * states are not (token weights enter the states as three bf16 limbs).  fp32, and other F, run
@@ -413,7 +413,7 @@ slay_status slay_decay_attn_bwd(const void* phq, const void* phk, const void* v,
  *         outside [0, n_slots), such as -1 for an idle row of the batch, is left out: nothing is
  *         read or written for it, and its out row stays as it was.  So is a row whose slot an
  *         earlier row of the call names.
- * No workspace. */
+ * Bt*H <= 2^27.  No workspace. */
 slay_status slay_decay_decode_step(const void* phq, const void* phk, const void* v,
                                    const float* log_decay, float* S, float* z,
                                    const int32_t* slots, void* out, int Bt, int H, int F, int Dv,
@@ -428,7 +428,7 @@ slay_status slay_decay_decode_step(const void* phq, const void* phk, const void*
  *         The two pools are one and the same or share no byte.  z_src, z_dst both NULL: no z.
  * src, dst : device [n] int32, n <= 4096.  A pair with src outside [-1, n_src) or dst outside
  *         [0, n_dst) is left out.
- * No workspace. */
+ * H*F <= 2^24.  No workspace. */
 slay_status slay_state_copy(const float* S_src, const float* z_src, const int32_t* src, int n_src,
                             float* S_dst, float* z_dst, const int32_t* dst, int n_dst, int n,
                             int H, int F, int Dv, void* stream);
