@@ -426,6 +426,7 @@ slay_status slay_decay_decode_step(const void* phq, const void* phk, const void*
  * slot more than once the last pair wins.
  * S_src, z_src : device [n_src,H,F,Dv], [n_src,H,F] fp32;  S_dst, z_dst : likewise n_dst slots.
  *         The two pools are one and the same or share no byte.  z_src, z_dst both NULL: no z.
+ *         With n_src == 0 the source is not read, and slots can only be cleared.
  * src, dst : device [n] int32, n <= 4096.  A pair with src outside [-1, n_src) or dst outside
  *         [0, n_dst) is left out.
  * H*F <= 2^24.  No workspace. */

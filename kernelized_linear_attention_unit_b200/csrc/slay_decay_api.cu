@@ -201,8 +201,10 @@ slay_status slay_state_copy(const float* S_src, const float* z_src, const int32_
         return SLAY_ERR_UNSUPPORTED;
     if (n == 0 || n_dst == 0) return SLAY_OK;
     if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4)) return SLAY_ERR_INVALID_ARG;
-    if (!tensor_ok(S_src) || !tensor_ok(S_dst) || (z_src == nullptr) != (z_dst == nullptr)) return SLAY_ERR_INVALID_ARG;
-    if (z_src && (!aligned(z_src, 16) || !aligned(z_dst, 16))) return SLAY_ERR_INVALID_ARG;
+    if (!tensor_ok(S_dst) || (z_dst && !aligned(z_dst, 16))) return SLAY_ERR_INVALID_ARG;
+    // (a source pool of no slots has no memory: the call only clears)
+    if (n_src > 0 && (!tensor_ok(S_src) || (z_src == nullptr) != (z_dst == nullptr) || (z_src && !aligned(z_src, 16))))
+        return SLAY_ERR_INVALID_ARG;
     const int64_t hf = static_cast<int64_t>(H) * F;
     // one pool, or two that share no byte
     auto overlap = [&](const float* p, const float* q, int64_t w) {

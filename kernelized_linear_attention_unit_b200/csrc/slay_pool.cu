@@ -272,8 +272,8 @@ cudaError_t state_copy(const CopyArgs& a, cudaStream_t st)
     const int64_t uS = a.hf * 16;
     const int wS = width(uS, 16);
     const int nS = static_cast<int>((uS + wS - 1) / wS);
-    const int z16 = a.z_src && a.hf % 4 == 0;
-    const int64_t uZ = a.z_src ? (z16 ? a.hf / 4 : a.hf) : 0;
+    const int z16 = a.z_dst && a.hf % 4 == 0;
+    const int64_t uZ = a.z_dst ? (z16 ? a.hf / 4 : a.hf) : 0;
     const int wZ = width(uZ, 16);
     const int nZ = static_cast<int>((uZ + wZ - 1) / wZ);
     const size_t stage = static_cast<size_t>(a.n) * std::max(wS, wZ) * 16;

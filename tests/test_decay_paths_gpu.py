@@ -289,3 +289,18 @@ def test_gradients_on_two_streams_with_blocks_of_their_own():
         torch.cuda.synchronize()
         for a, b in zip(alone, both):
             assert all(torch.equal(a[k], b[k]) for k in a)
+
+
+# ------------------------------------------------------------------------------- pool
+@gpu
+@pytest.mark.parametrize("with_z,F", [(True, 64), (True, 33), (False, 64)])
+def test_copy_from_a_pool_of_no_slots_clears(with_z, F):
+    g = base._gen(51)
+    S, z = base._randn(g, 5, 2, F, 64), base._randn(g, 5, 2, F)
+    S0, z0 = S.clone(), z.clone()
+    i = lambda *x: torch.tensor(x, device="cuda", dtype=torch.int32)  # noqa: E731
+    none_S, none_z = torch.empty(0, 2, F, 64, device="cuda"), torch.empty(0, 2, F, device="cuda")
+    bd.slay_state_copy(none_S, none_z if with_z else None, i(-1, 0, -1), S, z if with_z else None, i(3, 1, 0))
+    for pool, old, cleared in ((S, S0, True), (z, z0, with_z)):
+        for slot in range(5):
+            assert torch.equal(pool[slot], torch.zeros_like(old[slot]) if cleared and slot in (0, 3) else old[slot])
