@@ -258,8 +258,8 @@ __global__ void __launch_bounds__(kNT) k_dec_scan(Sweep s0, Sweep s1, int BH, in
     const Sweep& s = static_cast<int>(blockIdx.y) < BH ? s0 : s1;
     const int64_t bh = static_cast<int>(blockIdx.y) % BH;
     const int n = seq_len(s.lengths, static_cast<int>(bh / s.H), s.L);
-    const float g2 = s.log_decay[bh % s.H] * kLog2e;
-    const float lam_c = decay_pow(g2, kC);
+    const float g = s.log_decay[bh % s.H], g2 = g * kLog2e;
+    ChunkDecay lam_c(g, g2, kC);
     constexpr int kAhead = 8;
     auto walk = [&](auto* p, const auto* from, auto* to, int64_t w, int64_t x, auto zero, auto step) {
         auto run = from ? from[bh * w + x] : zero;
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kNT) k_dec_scan(Sweep s0, Sweep s1, int BH, in
                 const int c = s.rev ? s.nc - 1 - i0 - i : i0 + i;
                 p[c * w] = run;
                 const int nn = min(max(n - c * kC, 0), kC);
-                run = step(nn == kC ? lam_c : decay_pow(g2, nn), run, t[i]);
+                run = step(nn == kC ? lam_c.next() : decay_pow(g2, nn), run, t[i]);
             }
         }
         if (to) to[bh * w + x] = run;

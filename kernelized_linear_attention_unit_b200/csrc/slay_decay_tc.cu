@@ -869,9 +869,10 @@ __device__ __forceinline__ void sweep(const CUtensorMap& tfs, const CUtensorMap&
             warp_arrive(&bar[kMode == kState ? B_YF + eb : B_YF]);
         };
         // M <- lambda^n M + T
+        ChunkDecay lam_c(p.log_decay[bh % p.H], g2, kT);
         auto update_m = [&](int i) {
             const int n = min(kT, len - chunk_of(i) * kT);
-            const float lam = decay_pow(g2, n);
+            const float lam = n == kT ? lam_c.next() : decay_pow(g2, n);
             const bool two = kMode != kOutE && nl > 1;
             if (kMode != kState) {
                 wait_k(B_TF, i);

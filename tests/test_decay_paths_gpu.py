@@ -304,3 +304,52 @@ def test_copy_from_a_pool_of_no_slots_clears(with_z, F):
     for pool, old, cleared in ((S, S0, True), (z, z0, with_z)):
         for slot in range(5):
             assert torch.equal(pool[slot], torch.zeros_like(old[slot]) if cleared and slot in (0, 3) else old[slot])
+
+
+# ----------------------------------------------------------------- long and slow decays
+def _slow_decay(chunk, L):
+    """A decay over some 2^18 tokens whose factor of a chunk is about as far from a float as it can be."""
+    g = np.float32(-3e-6) - np.arange(512, dtype=np.float32) * np.float32(1e-9)
+    exact = np.exp(g.astype(np.float64) * chunk)
+    off = np.abs(exact.astype(np.float32).astype(np.float64) - exact)
+    return float(g[off.argmax()]), float(off.max()) * (L // chunk)
+
+
+@pytest.mark.parametrize("chunk", [64, 128])
+def test_a_fixed_factor_of_a_chunk_would_not_do(chunk):
+    """The state of 2^18 tokens, chunk by chunk in fp64, with the chunk's factor rounded once."""
+    L = 1 << 18
+    g, worst = _slow_decay(chunk, L)
+    own = np.exp(g * np.arange(chunk, dtype=np.float64)).sum()
+    off = []
+    for lam in (np.exp(g * chunk), float(np.float32(np.exp(g * chunk)))):
+        off.append(own * (1.0 - lam ** (L // chunk)) / (1.0 - lam))
+    assert worst > 2e-5 and abs(off[1] / off[0] - 1.0) > 1e-5, (worst, off)
+
+
+@gpu
+@pytest.mark.parametrize("dt,H", [("f32", 1), ("bf16", 80), ("bf16", 1)])
+def test_long_slow_decays_keep_their_states(dt, H):
+    """States, denominators and gradients of states over 2^18 tokens, at the bar of fp32 outputs:
+    the sequence in one walk on either path, and cut."""
+    L, F = 1 << 18, 8
+    g, _ = _slow_decay(64 if dt == "f32" else 128, L)
+    gen = base._gen(61)
+    one = lambda *s: base._randn(gen, 1, 1, L, *s)  # noqa: E731
+    q, k = (torch.exp(0.7 * one(F)).to(base.TDT[dt]) for _ in range(2))
+    v, do = ((1.0 + one(64)).to(base.TDT[dt]) for _ in range(2))
+    many = lambda x: x.expand(1, H, *x.shape[2:]).contiguous()  # noqa: E731
+    ld, out, den = torch.full((H,), g, device="cuda"), torch.empty_like(many(v)), torch.empty(1, H, L, device="cuda")
+    S, z = torch.empty(1, H, F, 64, device="cuda"), torch.empty(1, H, F, device="cuda")
+    bd.slay_kernel_status(bd.slay_decay_attn_fwd(many(q), many(k), many(v), ld, out, den=den, S_out=S, z_out=z))
+    t = torch.arange(L, device="cuda").double()
+    w = torch.exp(g * (L - 1 - t))[:, None] * k[0, 0].double()
+    up = torch.exp(g * (t + 1))[:, None] * q[0, 0].double()
+    want = {"S_out": w.T @ v[0, 0].double(), "z_out": w.sum(0), "dS_in": up.T @ do[0, 0].double()}
+    want["den"] = q[0, 0, -1].double() @ want["z_out"]
+    dS = torch.empty_like(S)
+    grads = [torch.empty_like(many(x)) for x in (q, k, v)]
+    bd.slay_kernel_status(bd.slay_decay_attn_bwd(many(q), many(k), many(v), ld, many(do), *grads, normalize=False, dS_in=dS))
+    for name, got in (("S_out", S[0, -1]), ("z_out", z[0, -1]), ("den", den[0, -1, -1]), ("dS_in", dS[0, -1])):
+        rel = float((got.double() - want[name]).norm() / want[name].norm())
+        assert rel <= 1e-5, (name, rel)
