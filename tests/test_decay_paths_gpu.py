@@ -353,3 +353,36 @@ def test_long_slow_decays_keep_their_states(dt, H):
     for name, got in (("S_out", S[0, -1]), ("z_out", z[0, -1]), ("den", den[0, -1, -1]), ("dS_in", dS[0, -1])):
         rel = float((got.double() - want[name]).norm() / want[name].norm())
         assert rel <= 1e-5, (name, rel)
+
+
+def _slow_step():
+    """A decay over some thousand tokens whose factor of one step is about as far from a float as it can be."""
+    g = np.float32(-1.0 / 1024) - np.arange(512, dtype=np.float32) * np.float32(1e-8)
+    exact = np.exp(g.astype(np.float64))
+    return float(g[np.abs(exact.astype(np.float32).astype(np.float64) - exact).argmax()])
+
+
+def test_a_fixed_factor_of_a_step_would_not_do():
+    g, n = _slow_step(), 4096
+    sums = [(1.0 - lam ** n) / (1.0 - lam) for lam in (np.exp(g), float(np.float32(np.exp(g))))]
+    assert abs(sums[1] / sums[0] - 1.0) > 2e-5
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_thousands_of_decode_steps_keep_their_states(dt):
+    """The states after 4096 steps, at the bar of fp32 outputs; heads without decay, with a slow one and with none left."""
+    H, F, n = 4, 32, 4096
+    gen = base._gen(62)
+    q, k = (torch.exp(0.7 * base._randn(gen, n, 1, H, F)).to(base.TDT[dt]) for _ in range(2))
+    v = (1.0 + base._randn(gen, n, 1, H, 64)).to(base.TDT[dt])
+    ld = torch.tensor([0.0, _slow_step(), -0.5, -math.inf], device="cuda")
+    S, z, out = torch.zeros(1, H, F, 64, device="cuda"), torch.zeros(1, H, F, device="cuda"), torch.empty_like(v[0])
+    for t in range(n):
+        bd.slay_decay_decode_step(q[t], k[t], v[t], ld, S, z, out, eps=1e-3)
+    w = torch.stack([ref.powers(g, torch.arange(n - 1, -1, -1, device="cuda")) for g in ld])[..., None]
+    kk, vv = k[:, 0].transpose(0, 1).double(), v[:, 0].transpose(0, 1).double()
+    want, want_z = (w * kk).transpose(1, 2) @ vv, (w * kk).sum(1)
+    for h in range(H):
+        assert float((S[0, h] - want[h]).norm() / want[h].norm()) <= 1e-5, h
+        assert float((z[0, h] - want_z[h]).norm() / want_z[h].norm()) <= 1e-5, h
