@@ -620,10 +620,19 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+# current_stream(device).cuda_stream without the object, 2 us of a small call, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_handle(device):
+    """The handle of `device`'s current stream."""
+    return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+
+
 def _call_on(device, stream, fn, name, args):
     """fn(*args, stream) with `device` current; stream: the caller's, or that device's current one."""
-    if stream is None:   # current_stream(device).cuda_stream without the object (2 us of a small call)
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    if stream is None:
+        raw = _current_handle(device)
     elif stream.device != device:
         raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
     else:

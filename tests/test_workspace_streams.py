@@ -82,3 +82,26 @@ def test_another_streams_call_takes_no_block_of_this_one():
     side.synchronize()
     assert ws.data_ptr() != at
     assert torch.equal(out, want)
+
+
+def test_current_stream_without_torchs_own_shortcut(monkeypatch):
+    """The handle comes from torch's public stream where its private shortcut is missing."""
+    asked = []
+    monkeypatch.setattr(bd, "_raw_stream", None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: asked.append(dev) or types.SimpleNamespace(cuda_stream=77))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    got = []
+    dev = torch.device("cuda", 3)
+    bd._call_on(dev, None, lambda *a: got.append(a) or bd.SLAY_OK, "call", (1, 2))
+    assert asked == [dev] and got == [(1, 2, 77)]
+
+
+@pytest.mark.gpu
+def test_current_stream_handles_agree(monkeypatch):
+    dev, side = torch.device("cuda", torch.cuda.current_device()), torch.cuda.Stream()
+    for stream in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(stream):
+            assert bd._current_handle(dev) == stream.cuda_stream
+            with monkeypatch.context() as m:
+                m.setattr(bd, "_raw_stream", None)
+                assert bd._current_handle(dev) == stream.cuda_stream
