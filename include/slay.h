@@ -350,8 +350,9 @@ slay_status slay_linear_attn_fwd(const void* phq, const void* phk, const void* v
  *   out_i = num_i / (den_i + eps) if normalize != 0, else num_i
  *   S_out = sum_j lambda^(n-1-j) phk_j v_j^T + lambda^n S_in,
  *   z_out = sum_j lambda^(n-1-j) phk_j       + lambda^n z_in
- * in O(L), by chunks with fp32 states.  With log_decay = 0 and normalize != 0 it is
- * slay_linear_attn_fwd(causal); normalize = 0 suits signed rows (plain queries and keys).
+ * in O(L), by chunks with fp32 states.  With log_decay = 0 and normalize != 0 it is the
+ * contraction of slay_linear_attn_fwd(causal), which rounds less in bf16 (below: its scores and
+ * states stay fp32); normalize = 0 suits signed rows (plain queries and keys).
  * phq, phk  : device [B,H,L,F] in dt;  v : device [B,H,L,Dv] in dt;  F <= 1024, Dv == 64.
  * log_decay : device [H] fp32, a constant of the model (there is no gradient for it).
  * lengths   : device [B] int32 or NULL (every sequence has L tokens): sequence b is its first
@@ -368,8 +369,10 @@ slay_status slay_linear_attn_fwd(const void* phq, const void* phk, const void* v
  * finite may reach every row of its 128-token chunk.  B*H <= 21845, L <= 4194240.
  * bf16 with F % 8 == 0, F <= 512 runs on tensor cores (SLAY_PATH_TC_CONTRACTION): fp32
  * accumulation; the masked scores and the state's operand are rounded to bf16, den and the
- * states are not (token weights enter the states as three bf16 limbs).  fp32, and other F, run
- * on CUDA cores in fp32. */
+ * states are not (token weights enter the states as three bf16 limbs).  A state that only its
+ * operand is read from takes two limbs, so out can differ in its last bit with S_out and without
+ * (and dv, of slay_decay_attn_bwd, with dS_in and without); calls alike repeat bit for bit.
+ * fp32, and other F, run on CUDA cores in fp32. */
 slay_status slay_decay_attn_fwd(const void* phq, const void* phk, const void* v,
                                 const float* log_decay, const int32_t* lengths,
                                 const float* S_in, const float* z_in, void* out, float* den,

@@ -555,9 +555,10 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr size_t kSmemS = 2 * 64 * kPitch * sizeof(float), kSmemO = 4 * 64 * kPitch * sizeof(float);
 // Up to this many CTAs, the outputs' kernels take half a chunk's queries each (R = 2): the
-// halves still find an SM each.  B1 H3 L512 F128 forward 20.5 us with halves against 22.8, with
-// 120 CTAs 30.8 / 34.9; but F64 22.6 / 20.5 there, and backward B1 H3 L512 F64 (72 CTAs)
-// 25.0 / 19.6, with 48 17.5 / 19.5.
+// halves still find an SM each.  B1 H3 L512 F128 forward (24 CTAs) 20.5 us with halves against 22.8
+// with whole chunks, backward B1 H2 F64 (48) 17.5 / 19.5; beyond, the features decide and the rule
+// takes the safer side: 120 CTAs forward F128 30.8 / 34.9, F64 22.6 / 20.5, backward F64 (72)
+// 25.0 / 19.6.
 constexpr int64_t kFew = 64;
 
 // The states of a sweep, or of two at once.

@@ -14,7 +14,7 @@
 // each, so an output sees two besides its own (the normalized dphq takes both in two limbs);
 // the decay weight of a token's state term is folded into the 64-wide side as w_j u_j = hi +
 // mid + lo, three bf16 limbs, where the fp32 state leaves the call, so that it is as exact as an
-// fp32 sum (one limb alone would be off by 2^-9), and two (2^-17) where only its bf16 copy is
+// fp32 sum (one limb alone would be off by up to 2^-8), and two (2^-16) where only its bf16 copy is
 // read.  The z column (the ones column of u) takes its weights as three bf16 columns of a
 // 16-wide operand, and so does the denominator's state part; the denominator's other part is
 // summed in fp32 from the scores.
@@ -25,9 +25,9 @@
 // 2 KB of B per 64 columns, 128 bytes a clock), 4000 of them for the 88 MMAs of a forward
 // chunk, which is why accumulators are as wide as tensor memory allows; P~ is read from tensor
 // memory.  The chain of a chunk (scores, masking, state sum, its bf16 copy, the next scores)
-// takes 8000 to 9000 clocks: forward B32 H12 L1024 F256 in 104 us, 4.9 TB/s, 74% of the copy
+// takes 8000 to 9000 clocks: forward B32 H12 L1024 F256 in 106 us, 4.8 TB/s, 73% of the copy
 // bandwidth (tensor pipe 32% active); with fewer (b, h) than SMs the sequence is cut into segments, whose sums
-// (k_tc_dec<kState>) read the F side once more.  Measured alternatives: 512 threads with four
+// (k_tc_dec<kState>) read the F side once more, at 54% of the DRAM peak (B1 H16 L16384 F256).  Measured alternatives: 512 threads with four
 // state warps in kOutF, too, 121 against 104 us; MMA loops not unrolled 126 us; roles chosen at
 // run time 162 us (the code outgrew the instruction cache).
 #include <cuda.h>
@@ -250,7 +250,7 @@ __device__ __forceinline__ void sweep(const CUtensorMap& tfs, const CUtensorMap&
     const bool leaves = p.last && (kMode == kState || seg == (kRev ? 0 : nseg - 1));
     auto chunk_of = [&](int i) { return rev ? c_lo + count - 1 - i : c_lo + i; };
     const float g2 = p.log_decay[bh % p.H] * kLog2e;
-    // limbs of the weighted rows: three where the fp32 state leaves the call, two (2^-17) where
+    // limbs of the weighted rows: three where the fp32 state leaves the call, two (2^-16) where
     // only its bf16 copy is read; without decay and row scalars the weights are 1, one is exact
     const bool has_z = kNorm && (kMode != kOutF || !kRev || p.z_state);
     const int nl = kMode == kState ? 3 : g2 == 0.0f && !kCols ? 1 : kMode == kOutF && leaves ? 3 : 2;
@@ -1356,7 +1356,7 @@ P base(const DecayArgs& a, const Plan& c, int* err, bool withhold)
 // F = 256) and the one that walks last writes the state; beyond, a scan kernel does both.  A
 // state that enters the walk counts as two more.  Forward at F = 256: four segments (B4 H8 L2048)
 // 40 us against 44 with the scan, nine (B1 H16 L16384) 128 against 118, three and a carried
-// state (B1 H4 L384) 22.6 against 18.5, two and one (B3 H24 L384) 28 against 31.
+// state (B1 H4 L384) 22.6 against 18.5.
 constexpr int kMaxSums = 4;
 
 // A walk whose segments' states are wanted.
@@ -1467,7 +1467,8 @@ cudaError_t launch_grads(const CUtensorMap& k, const CUtensorMap& v, const CUten
 // lengths even out, so do several waves of CTAs, and few CTAs fill each other's idle SMs.
 // Backward, apart and together: B8 H8 L1111 F128 ragged (in two segments) 69 and 59 us; B32 H12
 // L1024 F256 383 and 351; B1 H4 L1000 F256 41 and 27.  Where each fills most of the GPU once, they had better
-// follow one another: B8 H16 L1000 F128 122 apart, 127 together.
+// follow one another: B8 H16 L1000 F128 122 apart, 127 together.  (The host does not see the lengths: a
+// ragged batch whose sequences are all long takes the latter.)
 bool one_launch(const DecayArgs& a, int64_t n0, int64_t n1, int64_t n2)
 {
     return a.lengths || std::max(n0, n1) > kNumSMs || waves(n0 + n1 + n2) < waves(n0) + waves(n1) + waves(n2);

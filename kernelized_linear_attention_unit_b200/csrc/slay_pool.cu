@@ -178,7 +178,9 @@ cudaError_t decode_t(const DecodeArgs& a, cudaStream_t st)
 // the highest pair index.
 // B200: 128 slots of 2.1 MB (477 MB moved) in 90 us, 5.3 TB/s, 81% of the copy bandwidth.
 // Ranges of 512 bytes (64 KiB a CTA, three to an SM) measured best: 256 bytes 97 us, 1 KiB with
-// one CTA 94 us; bulk asynchronous copies of the same ranges 93 us in one stage or two.
+// one CTA 94 us; bulk asynchronous copies of the same ranges 93 us in one stage or two.  The range
+// shrinks as the pairs share a CTA's memory: 512 slots of 266 KB 63 us (4.3 TB/s), 2000 (32 bytes)
+// 766 us (1.4), 4096 (16 bytes) 3.4 ms (0.6); of 16.6 KB, 4096 slots 62 us (2.2).
 template <typename U>
 __device__ __forceinline__ void copy_columns(const U* src_base, U* dst_base, int64_t slot_units, int64_t c0, int wu,
                                              int n, const int* src, const int* dst, U* stage)
